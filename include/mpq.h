@@ -388,6 +388,133 @@ MPQ_API mpq_status mpq_stage_energy_noalloc(mpq_plan_t plan, const float* W, int
                                             const uint16_t* idx, float* w_hat, float* energy,
                                             mpq_stream_t stream);
 
+/* --------------------------------------- layers with solved weights --- */
+/* What a user runs around the solve: a model's layers with w_hat, to make the
+ * next layer's calibration rows ([Main experiments]) and the model's answers,
+ * and the comparison of those answers with the unquantised model's
+ * (perplexity is the paper's own measure).  These need no plan.  Beyond the
+ * conventions at the head of this file:
+ *  - Rows may be strided: `ld*` is the distance between rows in elements,
+ *    columns are contiguous; inputs need no alignment.  Outputs are
+ *    contiguous.  Outputs must not overlap inputs or each other.
+ *  - Work runs on the current device, which must own every buffer.  The calls
+ *    can be captured into graphs; scratch is the caller's (`workspace`, on a
+ *    256-byte boundary, size from the _workspace_bytes function for the same
+ *    arguments; 0: none is needed and NULL will do), so that calls on
+ *    different streams or in different graphs share nothing.
+ *  - Sums and statistics are fp32, in an order that does not change from run
+ *    to run; results are rounded once to the output's type. */
+typedef enum { MPQ_F32 = 0, MPQ_BF16 = 1, MPQ_F16 = 2 } mpq_dtype;
+typedef enum {
+  MPQ_ACT_NONE = 0,
+  MPQ_ACT_RELU = 1,
+  MPQ_ACT_GELU = 2,      /* z Phi(z)                                          */
+  MPQ_ACT_GELU_TANH = 3, /* z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))   */
+  MPQ_ACT_SILU = 4       /* z / (1 + e^-z)                                    */
+} mpq_act;
+
+/* y = act(z) + residual, z = x W^T + bias.
+ *   x: rows x k, weight: n x k (one row per output, the layout of w_hat),
+ *   both of `dtype` (MPQ_BF16 or MPQ_F16).  bias: n of dtype or MPQ_F32, may
+ *   be NULL.  residual: rows x n of y_dtype, may be NULL.  preact: out, rows x
+ *   n of dtype, z for the backward pass, may be NULL.  y: out, rows x n of
+ *   dtype or MPQ_F32 (which mpq_gram_accumulate reads).
+ *   0 <= rows <= 2^23, 1 <= n, k <= 2^22.  A workspace is needed only where x
+ *   or weight has a base or a row stride that is no multiple of 16 bytes, or
+ *   rows that overlap.
+ * The products run on the tensor cores with fp32 accumulation. */
+MPQ_API int64_t mpq_linear_workspace_bytes(const void* x, int64_t ldx, const void* weight, int64_t ldw,
+                                           int64_t rows, int64_t n, int64_t k);
+MPQ_API mpq_status mpq_linear(const void* x, int64_t ldx, const void* weight, int64_t ldw, int64_t rows,
+                              int64_t n, int64_t k, int32_t dtype, const void* bias, int32_t bias_dtype,
+                              int32_t act, const void* residual, int64_t ldr, void* preact, void* y,
+                              int32_t y_dtype, void* workspace, int64_t workspace_bytes,
+                              mpq_stream_t stream);
+
+/* Gradients of mpq_linear: with dz = dy * act'(preact),
+ *   dx = dz W (rows x k), dweight = dz^T x (n x k), both of dtype, dbias =
+ *   column sums of dz (n of dtype or MPQ_F32); each may be NULL (with the
+ *   solved weights frozen, dweight is).  The residual's gradient is dy.
+ *   preact: rows x n of dtype, as mpq_linear wrote it; not read (may be NULL)
+ *   for MPQ_ACT_NONE.  x is not read without dweight, weight not without dx.
+ *   dz is rounded to dtype for the tensor cores; dbias sums it unrounded.
+ *   rows = 0 leaves zeros in dweight and dbias. */
+MPQ_API int64_t mpq_linear_backward_workspace_bytes(const void* dy, int64_t ldy, const void* x, int64_t ldx,
+                                                    const void* weight, int64_t ldw, int64_t rows, int64_t n,
+                                                    int64_t k, int32_t act, int32_t need_dx,
+                                                    int32_t need_dweight, int32_t need_dbias);
+MPQ_API mpq_status mpq_linear_backward(const void* dy, int64_t ldy, const void* x, int64_t ldx,
+                                       const void* weight, int64_t ldw, const void* preact, int64_t ldz,
+                                       int64_t rows, int64_t n, int64_t k, int32_t dtype, int32_t act,
+                                       void* dx, void* dweight, void* dbias, int32_t dbias_dtype,
+                                       void* workspace, int64_t workspace_bytes, mpq_stream_t stream);
+
+/* Layer norm of every row: y = (x - mean) rstd * weight + bias, rstd =
+ * 1/sqrt(var + eps) with the population variance, taken around the mean.
+ *   x, y: rows x n of `dtype` (any mpq_dtype); weight, bias: n of dtype or
+ *   MPQ_F32 (`param_dtype`, one for both), each may be NULL (1 and 0).
+ *   mean, rstd: out, rows floats, for the backward pass, each may be NULL.
+ *   0 <= rows < 2^31, 1 <= n <= 2^20, eps > 0. */
+MPQ_API mpq_status mpq_layer_norm(const void* x, int64_t ldx, int64_t rows, int64_t n, int32_t dtype,
+                                  const void* weight, const void* bias, int32_t param_dtype, double eps,
+                                  void* y, float* mean, float* rstd, mpq_stream_t stream);
+
+/* Gradients of mpq_layer_norm, from the forward pass's mean and rstd: with
+ * xh = (x - mean) rstd and g = dy * weight,
+ *   dx = rstd (g - avg(g) - xh avg(g xh))  (rows x n of dtype),
+ *   dweight = sum over rows of dy xh, dbias = sum over rows of dy (n of
+ *   param_dtype); each may be NULL.  weight NULL: 1.
+ *   rows = 0 leaves zeros in dweight and dbias. */
+MPQ_API int64_t mpq_layer_norm_backward_workspace_bytes(int64_t rows, int64_t n, int32_t need_dparam);
+MPQ_API mpq_status mpq_layer_norm_backward(const void* dy, int64_t ldy, const void* x, int64_t ldx,
+                                           const float* mean, const float* rstd, int64_t rows, int64_t n,
+                                           int32_t dtype, const void* weight, int32_t param_dtype, void* dx,
+                                           void* dweight, void* dbias, void* workspace,
+                                           int64_t workspace_bytes, mpq_stream_t stream);
+
+/* Log probabilities of given tokens: with lse = log sum_i e^{l_i} of a row,
+ *   logprob = l_token - lse (0 for a token equal to ignore_index; NaN for any
+ *   other token outside [0, v)), entropy = -sum_i p_i log p_i, and the `top`
+ *   most likely alternatives, top_logprob descending with their ids in top_id
+ *   (equal logits: lowest id first).
+ *   logits: rows x v of `dtype`.  tokens: rows int64, or NULL (then logprob
+ *   must be NULL).  0 <= top <= min(v, MPQ_TOP_MAX); top_logprob, top_id: rows
+ *   x top, NULL for top = 0.  entropy may be NULL.
+ *   Logits of -inf and of the type's lowest value have probability 0.  A row
+ *   whose logits are all -inf has no distribution: logprob and top_logprob
+ *   are -inf, entropy 0.  A row with a NaN or +inf (or a logit above 2^127)
+ *   gives NaN, and top_id ranks its logits that are no NaN (-1 where there
+ *   are too few).
+ *   0 <= rows <= 2^24, 1 <= v <= 2^24. */
+#define MPQ_TOP_MAX 128
+MPQ_API mpq_status mpq_token_logprobs(const void* logits, int64_t ldl, int64_t rows, int64_t v, int32_t dtype,
+                                      const int64_t* tokens, int64_t ignore_index, int32_t top, float* logprob,
+                                      float* entropy, float* top_logprob, int64_t* top_id,
+                                      mpq_stream_t stream);
+
+/* Distillation from a teacher's top logits: with q = softmax(t / T) over the
+ * row's `top` teacher entries and p = softmax(l / T) over all v logits,
+ *   loss = sum_j q_j (log q_j - log p_{id_j})  (rows floats),
+ *   dlogits_i = weight / T (p_i - sum_{j: id_j = i} q_j)  (rows x v of dtype,
+ *   the gradient of sum over rows of weight * loss; may be NULL).
+ *   logits: rows x v of `dtype`.  top_logits: rows x top floats (logits or log
+ *   probabilities: a row's constant cancels), top_ids: rows x top int64, 1 <=
+ *   top <= MPQ_TOP_MAX.  weight: rows floats, NULL: 1.  T = temperature > 0.
+ *   An entry with a negative id is padding; one of -inf has q = 0.  An id met
+ *   twice adds both entries.  0.001 <= T <= 1000.  A row with no entry left, and every row of
+ *   weight 0, has gradient 0; the first also loss 0.  An id >= v makes its
+ *   row's loss and gradient NaN.
+ *   0 <= rows <= 2^24, 1 <= v <= 2^24. */
+MPQ_API mpq_status mpq_topk_distill(const void* logits, int64_t ldl, int64_t rows, int64_t v, int32_t dtype,
+                                    const float* top_logits, const int64_t* top_ids, int32_t top,
+                                    const float* weight, double temperature, float* loss, void* dlogits,
+                                    mpq_stream_t stream);
+
+/* Synchronise `stream`, read and clear the status of the layer operators on
+ * the current device: MPQ_OK, or MPQ_ERR_TIMEOUT when a bounded wait of a
+ * kernel ran out (its outputs are then undefined). */
+MPQ_API mpq_status mpq_ops_status(mpq_stream_t stream);
+
 /* ----------------------------------------------------------- profiling --- */
 /* Per-kernel timing with CUDA events recorded on the launching stream around
  * every kernel the library launches while profiling is on.  start clears

@@ -92,6 +92,17 @@ _sig("mpq_stage_vamp_scalar", ST, P, P, I64, P, P, P, P, P, P, P, P, P, P, P, P,
 _sig("mpq_stage_cd", ST, P, P, I64, P, P, P, I32, P, P)
 _sig("mpq_stage_energy", ST, P, P, I64, P, P, P, P, P, P)
 _sig("mpq_stage_energy_noalloc", ST, P, P, I64, P, P, P, P, P, P)
+F64 = C.c_double
+_sig("mpq_linear_workspace_bytes", I64, P, I64, P, I64, I64, I64, I64)
+_sig("mpq_linear", ST, P, I64, P, I64, I64, I64, I64, I32, P, I32, I32, P, I64, P, P, I32, P, I64, P)
+_sig("mpq_linear_backward_workspace_bytes", I64, P, I64, P, I64, P, I64, I64, I64, I64, I32, I32, I32, I32)
+_sig("mpq_linear_backward", ST, P, I64, P, I64, P, I64, P, I64, I64, I64, I64, I32, I32, P, P, P, I32, P, I64, P)
+_sig("mpq_layer_norm", ST, P, I64, I64, I64, I32, P, P, I32, F64, P, P, P, P)
+_sig("mpq_layer_norm_backward_workspace_bytes", I64, I64, I64, I32)
+_sig("mpq_layer_norm_backward", ST, P, I64, P, I64, P, P, I64, I64, I32, P, I32, P, P, P, P, I64, P)
+_sig("mpq_token_logprobs", ST, P, I64, I64, I64, I32, P, I64, I32, P, P, P, P, P)
+_sig("mpq_topk_distill", ST, P, I64, I64, I64, I32, P, P, I32, P, F64, P, P, P)
+_sig("mpq_ops_status", ST, P)
 _sig("mpq_profile_start", ST)
 _sig("mpq_profile_stop", ST, C.c_char_p, I64)
 _sig("mpq_last_error", C.c_char_p)
@@ -105,6 +116,9 @@ EXPORTED = ["mpq_params_default", "mpq_plan_create_from_spectrum", "mpq_plan_cre
             "mpq_solve_host", "mpq_stage_init", "mpq_stage_denoise", "mpq_stage_linear",
             "mpq_stage_vamp_scalar",
             "mpq_stage_cd", "mpq_stage_energy", "mpq_stage_energy_noalloc",
+            "mpq_linear_workspace_bytes", "mpq_linear", "mpq_linear_backward_workspace_bytes",
+            "mpq_linear_backward", "mpq_layer_norm", "mpq_layer_norm_backward_workspace_bytes",
+            "mpq_layer_norm_backward", "mpq_token_logprobs", "mpq_topk_distill", "mpq_ops_status",
             "mpq_profile_start", "mpq_profile_stop",
             "mpq_last_error", "mpq_kernel_launch_count"]
 

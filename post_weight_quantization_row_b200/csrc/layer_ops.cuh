@@ -1,0 +1,140 @@
+// Shared parts of the layer and answer operators (linear, layer norm, token
+// log probabilities, top-logits distillation): element types and vector access.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mpq_internal.cuh"
+
+namespace mpq {
+
+inline int64_t dtype_size(int32_t dt) { return dt == MPQ_F32 ? 4 : 2; }
+inline bool half_dtype(int32_t dt) { return dt == MPQ_BF16 || dt == MPQ_F16; }
+inline bool any_dtype(int32_t dt) { return dt == MPQ_F32 || half_dtype(dt); }
+
+// Index and SM count of the current device.
+mpq_status current_device(int* dev, int* sms);
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, const __nv_bfloat16*) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, const __half*) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16*) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __half*) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// W consecutive elements (W = 4 or 8) as floats.  vec: the address is aligned
+// to W elements (at most 16 bytes are read at once); otherwise one by one.
+template <int W, typename T>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[W], bool vec) {
+  if (!vec) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = to_f(p[i]);
+    return;
+  }
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + i);
+      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
+  } else if constexpr (W == 8) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2(w[i], p);
+      v[2 * i] = f.x; v[2 * i + 1] = f.y;
+    }
+  } else {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    const float2 a = unpack2(q.x, p), b = unpack2(q.y, p);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  }
+}
+template <int W, typename T>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[W], bool vec) {
+  if (!vec) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) p[i] = from_f<T>(v[i]);
+    return;
+  }
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else if constexpr (W == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1], p), pack2(v[2], v[3], p),
+                                              pack2(v[4], v[5], p), pack2(v[6], v[7], p));
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1], p), pack2(v[2], v[3], p));
+  }
+}
+// The same with the first n elements only (n < W at an edge); missing ones
+// read as zero.
+template <int W, typename T>
+__device__ __forceinline__ void load_edge(const T* p, float (&v)[W], int n, bool vec) {
+  if (n >= W) {
+    load_vec<W>(p, v, vec);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = i < n ? to_f(p[i]) : 0.0f;
+  }
+}
+template <int W, typename T>
+__device__ __forceinline__ void store_edge(T* p, const float (&v)[W], int n, bool vec) {
+  if (n >= W) {
+    store_vec<W>(p, v, vec);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < n) p[i] = from_f<T>(v[i]);
+  }
+}
+// A parameter vector (bias, norm weight) held in T or in fp32.
+template <int W, typename T>
+__device__ __forceinline__ void load_param(const void* p, bool f32, int64_t at, float (&v)[W],
+                                           int n, bool vec) {
+  if (f32) load_edge<W>(static_cast<const float*>(p) + at, v, n, vec);
+  else load_edge<W>(static_cast<const T*>(p) + at, v, n, vec);
+}
+template <int W, typename T>
+__device__ __forceinline__ void store_param(void* p, bool f32, int64_t at, const float (&v)[W],
+                                            int n, bool vec) {
+  if (f32) store_edge<W>(static_cast<float*>(p) + at, v, n, vec);
+  else store_edge<W>(static_cast<T*>(p) + at, v, n, vec);
+}
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x, 2 ulp; 0 below 2^-126
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+inline bool aligned_rows(const void* p, int64_t ld, int64_t elem, int64_t bytes) {
+  return ((uintptr_t)p % bytes) == 0 && (ld * elem) % bytes == 0;
+}
+
+}  // namespace mpq

@@ -1,0 +1,970 @@
+// linear: y = act(x W^T + b) + residual with bf16 or fp16 operands, and its
+// backward pass dz = dy * act'(z), dx = dz W, dW = dz^T x, db = sum dz.
+//
+// All three products run on tcgen05 (kind::f16, fp32 accumulators in TMEM)
+// with operands staged by TMA in the layout they have in memory: x W^T has
+// both operands contiguous along the contraction (K-major); dz W reads W with
+// its output index contiguous (MN-major), and dz^T x reads both so.  The
+// instruction and shared-memory descriptors take either order, so no operand
+// is transposed or copied.  Two kernels share the tile format (128-byte
+// swizzled boxes of 64 contiguous elements):
+//  - k_lin_pair: CTA pairs (cta_group::2), 256 x 256 tiles, persistent, two
+//    accumulators in TMEM so that a tile's epilogue overlaps the next tile's
+//    MMAs.  For products with tiles enough to fill the SMs.
+//  - k_lin_split: one 128 x (16..128) tile per cluster of S CTAs, each taking
+//    1/S of the contraction; the partial tiles are joined over distributed
+//    shared memory in a fixed order.  For few rows (one token: W is read once
+//    at HBM speed by tiles x S CTAs) and for small outputs.
+// The epilogue adds the bias, applies the activation, adds the residual and
+// rounds once, in fp32 before that.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "layer_ops.cuh"
+#include "tc_ptx.cuh"
+
+namespace mpq {
+namespace {
+using namespace tcx;
+
+// Set by a wait that ran out (mpq_ops_status reads and clears it).
+__device__ int g_lin_status;
+
+// ------------------------------------------------------------ activations --
+// gelu through erfc and the other two through 1/(1 + e^-u), so that small
+// results of large negative z keep their relative accuracy.
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case MPQ_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case MPQ_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case MPQ_ACT_GELU_TANH: {
+      const float u2 = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);  // 2 sqrt(2/pi) (...)
+      return __fdividef(z, 1.0f + __expf(-u2));
+    }
+    case MPQ_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == MPQ_ACT_NONE) return 1.0f;
+  if (act == MPQ_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  // beyond |z| = 30 the other three slopes are 0 or 1 to fp32; the clip keeps
+  // z^3 and e^-z finite (a NaN stays one)
+  const float c = z != z ? z : fminf(fmaxf(z, -30.0f), 30.0f);
+  if (act == MPQ_ACT_GELU)
+    return fmaf(0.3989422804014327f * c, expf(-0.5f * c * c), 0.5f * erfcf(-0.70710678118654752f * c));
+  float u = c, du = 1.0f;
+  if (act == MPQ_ACT_GELU_TANH) {
+    u = 1.5957691216057308f * fmaf(0.044715f * c * c, c, c);
+    du = 1.5957691216057308f * fmaf(0.134145f * c, c, 1.0f);
+  }
+  const float e = expf(-fabsf(u)), d = 1.0f / (1.0f + e);
+  const float s = u >= 0.0f ? d : e * d;  // 1/(1 + e^-u)
+  const float q = e * d * d;              // s (1 - s)
+  return fmaf(c * q, du, s);
+}
+
+// ------------------------------------------------------------- the operand --
+constexpr int BK = 64;              // contraction per stage
+constexpr int BOX = 64 * 64 * 2;    // bytes of a 64 x 64 box (8 KiB)
+
+// MN-major tile with 128-byte swizzle, as TMA writes boxes of 64 contiguous
+// output elements x 64 contraction rows: 8 contraction rows are 1024 B apart
+// (stride offset), the next 64 output elements one box further (leading
+// offset); 16 contraction rows further starts 2048 B on.
+__device__ __forceinline__ uint64_t mn128_desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(BOX >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+template <bool MN>
+__device__ __forceinline__ uint64_t op_desc(uint32_t base, int kk) {
+  return MN ? mn128_desc(base + (uint32_t)kk * 2048u) : sw128_desc(base + (uint32_t)kk * 32u);
+}
+// instruction descriptor: fp32 accumulator, A and B fp16 or bf16 (bits 7-9
+// and 10-12), MN-major flags (bits 15 and 16), N / 8 and M / 16
+template <typename T, bool A_MN, bool B_MN>
+__host__ __device__ constexpr uint32_t lin_idesc(int M, int N) {
+  const uint32_t f = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+struct LinOut {
+  const void* bias;      // n values in T or fp32, or NULL
+  const void* residual;  // rows x n in the output's type, or NULL
+  void* preact;          // rows x n in T, or NULL
+  void* out;             // rows x n
+  int64_t ldr, ldo;
+  int rows, cols, act;
+  bool bias_f32, bias_vec, res_vec, out_vec;
+};
+
+// One run of W consecutive columns of a row: bias, activation, residual, store.
+template <int W, typename T, typename O>
+__device__ __forceinline__ void lin_finish(const LinOut& o, int row, int col, float (&v)[W],
+                                           const float (&bias)[W]) {
+  const int n = o.cols - col;
+  const int64_t at = (int64_t)row * o.ldo + col;
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] += bias[i];
+  if (o.preact) store_edge<W>(static_cast<T*>(o.preact) + at, v, n, o.out_vec);
+  if (o.act != MPQ_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = act_value(v[i], o.act);
+  }
+  if (o.residual) {
+    float r[W];
+    load_edge<W>(static_cast<const O*>(o.residual) + (int64_t)row * o.ldr + col, r, n, o.res_vec);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] += r[i];
+  }
+  store_edge<W>(static_cast<O*>(o.out) + at, v, n, o.out_vec);
+}
+
+// ----------------------------------------------------------- CTA-pair GEMM --
+constexpr int PT = 256;                    // tile: 256 rows x 256 columns
+constexpr int P_STAGES = 6;
+constexpr int P_STAGE = 2 * 128 * BK * 2;  // 128 rows of A and 128 of B per CTA
+constexpr int P_EPI = 8;                   // epilogue warps
+constexpr int P_THREADS = 32 * (2 + P_EPI);
+constexpr int P_SMEM = P_STAGES * P_STAGE + P_EPI * 4096 + 1024 + 256;
+static_assert(P_SMEM <= 232448, "pair kernel's shared memory");
+
+// The walk over tiles: whole waves of 256 x 256 tiles, the rest of them as
+// two 128-column halves each, so that a last partial wave takes half as long.
+struct Walk {
+  int mt, nt, whole, total;
+};
+__device__ __forceinline__ Walk make_walk(int rows, int cols, int workers) {
+  Walk w;
+  w.mt = (rows + PT - 1) / PT;
+  w.nt = (cols + PT - 1) / PT;
+  const int t = w.mt * w.nt;
+  w.whole = t / workers * workers;
+  w.total = w.whole + 2 * (t - w.whole);
+  return w;
+}
+// Tiles run in groups of 8 row tiles (rows fastest), so that the panels of
+// both operands in flight stay in L2.
+__device__ __forceinline__ void walk_tile(const Walk& w, int t, int& m0, int& n0, int& wn) {
+  int s = t, half = 0;
+  wn = PT;
+  if (t >= w.whole) {
+    s = w.whole + (t - w.whole) / 2;
+    half = (t - w.whole) & 1;
+    wn = PT / 2;
+  }
+  const int per = 8 * w.nt, g = s / per, q = s % per;
+  const int gm = min(8, w.mt - g * 8);
+  m0 = (g * 8 + q % gm) * PT;
+  n0 = (q / gm) * PT + half * (PT / 2);
+}
+
+template <typename T, typename O, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(P_THREADS, 1)
+    k_lin_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+               int KC, const __grid_constant__ LinOut o) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* stg_all = smem + P_STAGES * P_STAGE;
+  uint64_t* full = (uint64_t*)(stg_all + P_EPI * 4096);
+  uint64_t* empty = full + P_STAGES;
+  uint64_t* tm_full = empty + P_STAGES;
+  uint64_t* tm_empty = tm_full + 2;
+  uint32_t* tmem_slot = (uint32_t*)(tm_empty + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // rank 0 issues the pair's MMAs
+  const int worker = (int)cluster_id_x(), nworkers = (int)(gridDim.x / 2);
+  const Walk walk = make_walk(o.rows, o.cols, nworkers);
+  const int KT = (KC + BK - 1) / BK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tm_full[b], 1);
+      mbar_init(&tm_empty[b], 2 * P_EPI);  // the epilogue warps of both CTAs
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(2 * PT));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any remote use
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t full_r0 = map_to_rank(smem_u32(full), 0);
+  const uint32_t tm_empty_r0 = map_to_rank(smem_u32(tm_empty), 0);
+
+  if (warp == 0 && lane == 0) {
+    // -------------------------------------------------------------- producer
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = worker; t < walk.total && ok; t += nworkers) {
+      int m0, n0, wn;
+      walk_tile(walk, t, m0, n0, wn);
+      const int am = m0 + (int)rank * 128;
+      const int bn = n0 + (int)rank * (wn / 2);
+      const uint32_t bytes = (uint32_t)((128 + wn / 2) * BK * 2);
+      for (int kt = 0; kt < KT; ++kt, ++it) {
+        const int s = it % P_STAGES;
+        if (it >= (uint32_t)P_STAGES && !mbar_wait(&empty[s], (it / P_STAGES - 1) & 1)) {
+          atomicOr(&g_lin_status, STATUS_TIMEOUT);
+          ok = false;
+          break;
+        }
+        uint8_t* a = smem + s * P_STAGE;
+        uint8_t* b = a + 128 * BK * 2;
+        const uint32_t fb = full_r0 + 8u * (uint32_t)s;  // rank 0's barrier counts both CTAs' bytes
+        if (rank == 0) mbar_expect_tx(&full[s], 2 * bytes);
+        const int k0 = kt * BK;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (A_MN) tma_load_2d_cg2(&ta, fb, a + h * BOX, am + h * 64, k0);
+          else tma_load_2d_cg2(&ta, fb, a + h * BOX, k0, am + h * 64);
+        }
+        for (int h = 0; h < wn / 128; ++h) {
+          if (B_MN) tma_load_2d_cg2(&tb, fb, b + h * BOX, bn + h * 64, k0);
+          else tma_load_2d_cg2(&tb, fb, b + h * BOX, k0, bn + h * 64);
+        }
+      }
+    }
+    // every copy lands before the CTA leaves (rank 0's barriers count both
+    // CTAs' copies; rank 1 waits for rank 0 at the closing cluster barrier)
+    if (rank == 0)
+      for (uint32_t q = (it > (uint32_t)P_STAGES ? it - P_STAGES : 0); q < it; ++q)
+        for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&full[q % P_STAGES], (q / P_STAGES) & 1); ++i)
+          if (i > 256) __nanosleep(64);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t ID_W = lin_idesc<T, A_MN, B_MN>(256, PT), ID_N = lin_idesc<T, A_MN, B_MN>(256, PT / 2);
+    uint32_t it = 0, tl = 0;
+    bool ok = true;
+    for (int t = worker; t < walk.total && ok; t += nworkers, ++tl) {
+      const int buf = tl & 1;
+      int m0, n0, wn;
+      walk_tile(walk, t, m0, n0, wn);
+      const uint32_t idesc = wn == PT ? ID_W : ID_N;
+      if (tl >= 2 && !mbar_wait_cl(&tm_empty[buf], (tl / 2 - 1) & 1)) {
+        atomicOr(&g_lin_status, STATUS_TIMEOUT);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)buf * PT;
+      for (int kt = 0; kt < KT; ++kt, ++it) {
+        const int s = it % P_STAGES;
+        if (!mbar_wait_cl(&full[s], (it / P_STAGES) & 1)) {
+          atomicOr(&g_lin_status, STATUS_TIMEOUT);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + s * P_STAGE), b = a + 128 * BK * 2;
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          umma_f16_cg2(d, op_desc<A_MN>(a, kk), op_desc<B_MN>(b, kk), idesc, (kt | kk) != 0 ? 1u : 0u);
+        umma_commit_cg2(smem_u32(&empty[s]));
+        umma_commit_cg2(map_to_rank(smem_u32(&empty[s]), 1));
+      }
+      if (ok) {
+        umma_commit_cg2(smem_u32(&tm_full[buf]));
+        umma_commit_cg2(map_to_rank(smem_u32(&tm_full[buf]), 1));
+      }
+    }
+    for (uint32_t q = (tl > 2 ? tl - 2 : 0); q < tl; ++q)  // MMAs finish before TMEM is freed
+      for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&tm_full[q & 1], (q / 2) & 1); ++i)
+        if (i > 256) __nanosleep(64);
+  } else if (warp >= 2) {
+    // -------------------------------------------------------------- epilogue
+    // two warps per TMEM lane quadrant, alternating over 32-column chunks.  A
+    // chunk goes through a swizzled 32 x 32 fp32 staging tile, which turns
+    // the lane-per-row layout into 8 consecutive columns per lane.
+    const int q = warp & 3, side = (warp - 2) >> 2;
+    float4* stg = reinterpret_cast<float4*>(stg_all + (warp - 2) * 4096);
+    const int c8 = (lane & 3) * 8, r8 = lane >> 2;
+    uint32_t tl = 0;
+    for (int t = worker; t < walk.total; t += nworkers, ++tl) {
+      const int buf = tl & 1;
+      const bool ok = __all_sync(0xffffffffu, mbar_wait_cl(&tm_full[buf], (tl / 2) & 1));
+      if (!ok) {
+        if (lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      int m0, n0, wn;
+      walk_tile(walk, t, m0, n0, wn);
+      const int row0 = m0 + (int)rank * 128 + q * 32;
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)buf * PT;
+      for (int c0 = side * 32; c0 < wn; c0 += 64) {
+        uint32_t v[32];
+        tmem_ld32(tbase + (uint32_t)c0, v);
+        if (c0 + 64 >= wn) {  // this warp's part is read: hand the accumulator back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);
+        }
+        const int col = n0 + c0 + c8;
+        if (n0 + c0 >= o.cols) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          stg[lane * 8 + (k ^ (lane & 7))] =
+              make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                          __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+        __syncwarp();
+        float bias[8] = {};
+        if (o.bias && col < o.cols)
+          load_param<8, T>(o.bias, o.bias_f32, col, bias, o.cols - col, o.bias_vec);
+        if (col < o.cols) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = i * 8 + r8;
+            if (row0 + rr < o.rows) {
+              const float4 x0 = stg[rr * 8 + ((c8 / 4) ^ (rr & 7))];
+              const float4 x1 = stg[rr * 8 + ((c8 / 4 + 1) ^ (rr & 7))];
+              float w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+              lin_finish<8, T, O>(o, row0 + rr, col, w, bias);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no peer still reads this CTA's memory or barriers
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * PT));
+  }
+}
+
+// -------------------------------------------------------------- split GEMM --
+// Roles are swapped: the operand with the output's columns (W, or x for dW)
+// fills the 128 TMEM lanes, the one with its rows (the tokens) the NT columns
+// of the accumulator, so few rows waste no tensor work.
+constexpr int S_THREADS = 192;
+
+struct SplitGeom {
+  int NT;      // rows of the output per tile (accumulator columns)
+  int stages;
+  int S;       // CTAs per cluster, each with its share of the contraction
+  int KT;      // contraction steps in all
+  uint32_t tmem_cols;
+};
+__host__ __device__ inline int split_stage_bytes(int NT) { return 128 * BK * 2 + NT * BK * 2; }
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <typename T, typename O, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(S_THREADS)
+    k_lin_split(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                const __grid_constant__ SplitGeom g, const __grid_constant__ LinOut o) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int stage = split_stage_bytes(g.NT);
+  uint64_t* full = (uint64_t*)(smem + g.stages * stage);
+  uint64_t* empty = full + g.stages;
+  uint64_t* done = empty + g.stages;
+  uint32_t* tmem_slot = (uint32_t*)(done + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = g.S > 1 ? (int)cluster_ctarank() : 0;
+  const int a0 = blockIdx.y * 128, b0 = blockIdx.z * g.NT;
+  const int k_lo = (int)((int64_t)g.KT * rank / g.S), k_hi = (int)((int64_t)g.KT * (rank + 1) / g.S);
+  const int nk = k_hi - k_lo;  // >= 1
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < g.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(g.tmem_cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  bool ok = true;
+  if (warp == 0 && lane == 0) {
+    int i = 0;
+    for (; i < nk; ++i) {
+      const int s = i % g.stages;
+      if (i >= g.stages && !mbar_wait(&empty[s], (i / g.stages - 1) & 1)) {
+        atomicOr(&g_lin_status, STATUS_TIMEOUT);
+        break;
+      }
+      uint8_t* a = smem + s * stage;
+      uint8_t* b = a + 128 * BK * 2;
+      const int k0 = (k_lo + i) * BK;
+      mbar_expect_tx(&full[s], (uint32_t)stage);
+      if (A_MN) {
+        tma_load_2d(&ta, &full[s], a, a0, k0);
+        tma_load_2d(&ta, &full[s], a + BOX, a0 + 64, k0);
+      } else {
+        tma_load_2d(&ta, &full[s], a, k0, a0);
+      }
+      if (B_MN) {
+        for (int h = 0; h < g.NT / 64; ++h) tma_load_2d(&tb, &full[s], b + h * BOX, b0 + h * 64, k0);
+      } else {
+        tma_load_2d(&tb, &full[s], b, k0, b0);
+      }
+    }
+    for (int q = (i > g.stages ? i - g.stages : 0); q < i; ++q)  // every copy lands
+      for (uint32_t w = 0; w < (1u << 25) && !mbar_try_wait(&full[q % g.stages], (q / g.stages) & 1); ++w)
+        if (w > 256) __nanosleep(64);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = lin_idesc<T, A_MN, B_MN>(128, g.NT);
+    for (int i = 0; i < nk; ++i) {
+      const int s = i % g.stages;
+      if (!mbar_wait(&full[s], (i / g.stages) & 1)) {
+        atomicOr(&g_lin_status, STATUS_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t a = smem_u32(smem + s * stage), b = a + 128 * BK * 2;
+#pragma unroll
+      for (int kk = 0; kk < BK / 16; ++kk)
+        umma_f16(tmem, op_desc<A_MN>(a, kk), op_desc<B_MN>(b, kk), idesc, (i | kk) != 0 ? 1u : 0u);
+      umma_commit(&empty[s]);
+    }
+    umma_commit(done);
+    for (uint32_t w = 0; w < (1u << 25) && !mbar_try_wait(done, 0); ++w)
+      if (w > 256) __nanosleep(64);
+  } else if (warp >= 2) {
+    ok = __all_sync(0xffffffffu, mbar_wait(done, 0));
+    if (!ok && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+  }
+  // All copies have landed and all MMAs have read them: the ring becomes the
+  // partial tile part[row][128 columns] (fp32).  Lane l of quadrant q holds
+  // column 32 q + l of the output, one row per accumulator column.
+  __syncthreads();
+  tc_fence_after();
+  float* part = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+    const int q = warp & 3;
+    const int nrow = min(g.NT, o.rows - b0);
+    for (int c0 = 0; c0 < nrow; c0 += 16) {
+      uint32_t v[16];
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+          "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+            "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+            "=r"(v[14]), "=r"(v[15])
+          : "r"(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0));
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c0 + j < nrow) part[(c0 + j) * 128 + q * 32 + lane] = __uint_as_float(v[j]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (g.S > 1) cluster_sync();  // every CTA's partial tile is written
+  {
+    // each CTA joins its share of the tile, in rank order, 4 columns a thread
+    const int nrow = min(g.NT, o.rows - b0);
+    const int units = nrow * 32;
+    const int u_hi = (int)((int64_t)units * (rank + 1) / g.S);
+    for (int u = (int)((int64_t)units * rank / g.S) + (int)threadIdx.x; u < u_hi; u += S_THREADS) {
+      const int r = u >> 5, c = (u & 31) * 4;
+      if (a0 + c >= o.cols) continue;
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const uint32_t at = smem_u32(part + r * 128 + c);
+      if (g.S > 1) {
+        for (int p = 0; p < g.S; ++p) {
+          const float4 x = ld_cluster4(map_to_rank(at, (uint32_t)p));
+          v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        }
+      } else {
+        const float4 x = *reinterpret_cast<const float4*>(part + r * 128 + c);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      }
+      float bias[4] = {};
+      if (o.bias) load_param<4, T>(o.bias, o.bias_f32, a0 + c, bias, o.cols - (a0 + c), o.bias_vec);
+      lin_finish<4, T, O>(o, b0 + r, a0 + c, v, bias);
+    }
+  }
+  __syncthreads();
+  if (g.S > 1) cluster_sync();  // no peer still reads this CTA's tile
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
+  }
+}
+
+// -------------------------------------------------- rows and pre-activation --
+// Copies rows x cols 16-bit elements to a leading dimension that TMA can take
+// (a multiple of 8).  Only for operands whose base or row stride is not a
+// multiple of 16 bytes.
+__global__ void k_lin_pack(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
+                           uint16_t* __restrict__ dst, int64_t ldd) {
+  const int64_t groups = ldd / 8;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * groups;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t r = i / groups, c = (i % groups) * 8;
+    uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? src[r * ld + c + j] : (uint16_t)0;
+    *reinterpret_cast<uint4*>(dst + r * ldd + c) = *reinterpret_cast<const uint4*>(v);
+  }
+}
+
+// dz = dy * act'(z), rounded to the operands' type for the tensor cores (half
+// a step of that type per element, which the products' sums average; dbias
+// sums the unrounded values), and per block of 64 rows the column sums.
+constexpr int DZ_ROWS = 64;
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_lin_dz(const T* __restrict__ dy, int64_t ldy, const T* __restrict__ z, int64_t ldz, int act,
+             int64_t rows, int64_t n, T* __restrict__ dz, int64_t ldd, float* __restrict__ part,
+             bool vec_y, bool vec_z) {
+  __shared__ float red[8][256 + 8];
+  const int cg = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.y * 256 + cg * 8;
+  const int64_t r_lo = (int64_t)blockIdx.x * DZ_ROWS, r_hi = min(rows, r_lo + DZ_ROWS);
+  float sum[8] = {};
+  if (c < n) {
+    const int left = (int)min((int64_t)8, n - c);
+    for (int64_t r = r_lo + rl; r < r_hi; r += 8) {
+      float g[8];
+      load_edge<8>(dy + r * ldy + c, g, left, vec_y);
+      if (act != MPQ_ACT_NONE) {
+        float u[8];
+        load_edge<8>(z + r * ldz + c, u, left, vec_z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] *= act_slope(u[j], act);
+      }
+      if (dz) store_vec<8>(dz + r * ldd + c, g, true);  // ldd is a multiple of 8: the pad is zero
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += g[j];
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[rl][cg * 8 + j] = sum[j];
+  __syncthreads();
+  const int64_t col = (int64_t)blockIdx.y * 256 + threadIdx.x;
+  if (col < n) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
+    part[(int64_t)blockIdx.x * n + col] = s;
+  }
+}
+
+// Column sums of `blocks` partial rows, in a fixed order.
+template <typename O>
+__global__ void __launch_bounds__(256)
+    k_lin_colsum(const float* __restrict__ part, int64_t blocks, int64_t n, O* __restrict__ out) {
+  __shared__ float red[8][32];
+  const int cl = threadIdx.x & 31, bl = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
+  float s = 0.0f;
+  if (c < n)
+    for (int64_t b = bl; b < blocks; b += 8) s += part[b * n + c];
+  red[bl][cl] = s;
+  __syncthreads();
+  if (bl == 0 && c < n) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += red[i][cl];
+    out[c] = from_f<O>(t);
+  }
+}
+
+// -------------------------------------------------------------------- host --
+PFN_cuTensorMapEncodeTiled_v12000 g_lin_encode = nullptr;
+std::mutex g_lin_mu;
+struct LinDevice {
+  bool ready = false;
+  int pairs = 0;
+};
+LinDevice g_lin_dev[64];
+
+mpq_status encode_box(CUtensorMap* tm, const void* base, int64_t inner, int64_t rows, int64_t ld,
+                      bool bf16, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  const CUresult r = g_lin_encode(
+      tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+      const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(MPQ_ERR_CUDA, "linear: cuTensorMapEncodeTiled failed with code " + std::to_string((int)r));
+  return MPQ_OK;
+}
+
+// An operand in memory: `rows` rows of `inner` contiguous elements.
+struct Operand {
+  const void* p;
+  int64_t inner, rows, ld;
+};
+bool tma_ok(const void* p, int64_t inner, int64_t rows, int64_t ld) {
+  return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (ld % 8 == 0 && ld >= inner));
+}
+int64_t packed_bytes(int64_t inner, int64_t rows) {
+  return round_up(rows * round_up(inner, 8) * 2, 256);
+}
+// A row stride for TMA where there is one row (its stride is not read).
+int64_t tma_ld(const Operand& a) { return a.rows <= 1 ? round_up(a.inner, 8) : a.ld; }
+
+mpq_status pack(Operand* a, void* dst, cudaStream_t st) {
+  const int64_t ldd = round_up(a->inner, 8), work = a->rows * (ldd / 8);
+  {
+    ProfScope ps_("k_lin_pack", st);
+    k_lin_pack<<<(unsigned)std::min<int64_t>(cdiv(work, 256), 148 * 16), 256, 0, st>>>(
+        static_cast<const uint16_t*>(a->p), a->ld, a->rows, a->inner, static_cast<uint16_t*>(dst), ldd);
+  }
+  count_launch();
+  a->p = dst;
+  a->ld = ldd;
+  return check_launch("k_lin_pack");
+}
+
+template <typename T, typename O, bool RN, bool CN>
+mpq_status set_attrs() {
+  MPQ_CUDA(cudaFuncSetAttribute(k_lin_pair<T, O, RN, CN>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
+  MPQ_CUDA(cudaFuncSetAttribute(k_lin_split<T, O, CN, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                113 * 1024));
+  return MPQ_OK;
+}
+
+mpq_status lin_device(int* dev_out, int* sms_out) {
+  int dev = 0;
+  MPQ_TRY(current_device(&dev, sms_out));
+  std::lock_guard<std::mutex> lk(g_lin_mu);
+  if (!g_lin_encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn)
+      return fail(MPQ_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    g_lin_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  if (!g_lin_dev[dev].ready) {
+    using B = __nv_bfloat16;
+    using H = __half;
+    MPQ_TRY((set_attrs<B, B, false, false>()));
+    MPQ_TRY((set_attrs<B, float, false, false>()));
+    MPQ_TRY((set_attrs<B, B, false, true>()));
+    MPQ_TRY((set_attrs<B, B, true, true>()));
+    MPQ_TRY((set_attrs<H, H, false, false>()));
+    MPQ_TRY((set_attrs<H, float, false, false>()));
+    MPQ_TRY((set_attrs<H, H, false, true>()));
+    MPQ_TRY((set_attrs<H, H, true, true>()));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)*sms_out);
+    cfg.blockDim = dim3(P_THREADS);
+    cfg.dynamicSmemBytes = P_SMEM;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int nc = 0;
+    if (cudaOccupancyMaxActiveClusters(&nc, k_lin_pair<B, B, false, false>, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      nc = 0;
+    }
+    g_lin_dev[dev].pairs = nc;
+    g_lin_dev[dev].ready = true;
+  }
+  *dev_out = dev;
+  return MPQ_OK;
+}
+
+// out[rows x cols] = R C^T over KC, the epilogue as `o` says.  RN / CN: the
+// operand that gives the output's rows / columns is stored with that index
+// contiguous (else with the contraction contiguous).
+template <typename T, typename O, bool RN, bool CN>
+mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const LinOut& o, cudaStream_t st,
+                       const char* tag) {
+  int dev = 0, sms = 0;
+  MPQ_TRY(lin_device(&dev, &sms));
+  constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+  const int64_t KT = cdiv(KC, BK);
+  const int64_t big = cdiv(o.rows, PT) * cdiv(o.cols, PT);
+  const int pairs = g_lin_dev[dev].pairs;
+  ProfScope ps_(tag, st);
+  if (pairs > 0 && o.rows > 128 && big * 2 >= pairs) {
+    CUtensorMap ta, tb;
+    MPQ_TRY(encode_box(&ta, R.p, R.inner, R.rows, tma_ld(R), bf, 64));
+    MPQ_TRY(encode_box(&tb, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, 64));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(2 * big, pairs));
+    cfg.blockDim = dim3(P_THREADS);
+    cfg.dynamicSmemBytes = P_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    MPQ_CUDA(cudaLaunchKernelEx(&cfg, k_lin_pair<T, O, RN, CN>, ta, tb, (int)KC, o));
+  } else {
+    SplitGeom g;
+    g.NT = RN ? (o.rows <= 64 ? 64 : 128) : (int)std::min<int64_t>(128, round_up(o.rows, 16));
+    const int64_t at_ = cdiv(o.cols, 128), bt = cdiv(o.rows, g.NT);
+    if (bt > 65535 || at_ > 65535) return fail(MPQ_ERR_INVALID_ARG, "linear: too many tiles");
+    g.S = 1;
+    while (g.S < 8 && at_ * bt * g.S * 2 <= 2 * sms && KT >= 4 * g.S) g.S *= 2;
+    g.KT = (int)KT;
+    const int budget = 111 * 1024;
+    g.stages = (int)std::min<int64_t>(budget / split_stage_bytes(g.NT), std::max<int64_t>(cdiv(KT, g.S), 1));
+    // the ring must also hold the partial tile
+    g.stages = std::max(g.stages, (int)cdiv(g.NT * 128 * 4, split_stage_bytes(g.NT)));
+    g.tmem_cols = 32;
+    while ((int)g.tmem_cols < g.NT) g.tmem_cols *= 2;
+    const int smem = g.stages * split_stage_bytes(g.NT) + (2 * g.stages + 1) * 8 + 16 + 1024;
+    CUtensorMap ta, tb;
+    MPQ_TRY(encode_box(&ta, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
+    MPQ_TRY(encode_box(&tb, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : g.NT));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)g.S, (unsigned)at_, (unsigned)bt);
+    cfg.blockDim = dim3(S_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)g.S;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    MPQ_CUDA(cudaLaunchKernelEx(&cfg, k_lin_split<T, O, CN, RN>, ta, tb, g, o));
+  }
+  count_launch();
+  return check_launch(tag);
+}
+
+mpq_status check_dims(const char* who, int64_t rows, int64_t n, int64_t k, int32_t dtype, int32_t act) {
+  if (rows < 0 || rows > (1 << 23) || n < 1 || n > (1 << 22) || k < 1 || k > (1 << 22))
+    return fail(MPQ_ERR_INVALID_ARG, std::string(who) + ": need 0 <= rows <= 2^23, 1 <= n, k <= 2^22");
+  if (!half_dtype(dtype)) return fail(MPQ_ERR_INVALID_ARG, std::string(who) + ": operands must be bf16 or fp16");
+  if (act < MPQ_ACT_NONE || act > MPQ_ACT_SILU)
+    return fail(MPQ_ERR_INVALID_ARG, std::string(who) + ": unknown activation");
+  return MPQ_OK;
+}
+
+template <typename T, typename O>
+mpq_status linear_fwd(Operand x, Operand w, const LinOut& o, char* ws, cudaStream_t st) {
+  if (!tma_ok(x.p, x.inner, x.rows, x.ld)) {
+    MPQ_TRY(pack(&x, ws, st));
+    ws += packed_bytes(x.inner, x.rows);
+  }
+  if (!tma_ok(w.p, w.inner, w.rows, w.ld)) MPQ_TRY(pack(&w, ws, st));
+  return lin_product<T, O, false, false>(x, w, x.inner, o, st, "k_linear");
+}
+
+struct BackPlan {  // workspace of a backward pass, in order
+  bool make_dz, pack_x, pack_w, sums;
+  int64_t dz, x, w, part, total;
+};
+BackPlan back_plan(const void* dy, int64_t ldy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                   int64_t rows, int64_t n, int64_t k, int32_t act, bool need_dx, bool need_dw, bool need_db) {
+  BackPlan p{};
+  const bool prod = need_dx || need_dw;
+  p.make_dz = prod && (act != MPQ_ACT_NONE || !tma_ok(dy, n, rows, ldy));
+  p.pack_x = need_dw && !tma_ok(x, k, rows, ldx);
+  p.pack_w = need_dx && !tma_ok(w, k, n, ldw);
+  p.sums = need_db;
+  p.dz = 0;
+  p.x = p.dz + (p.make_dz ? packed_bytes(n, rows) : 0);
+  p.w = p.x + (p.pack_x ? packed_bytes(k, rows) : 0);
+  p.part = p.w + (p.pack_w ? packed_bytes(k, n) : 0);
+  p.total = p.part + (p.sums ? round_up(cdiv(rows, DZ_ROWS) * n * 4, 256) : 0);
+  return p;
+}
+
+template <typename T>
+mpq_status linear_bwd(const void* dy, int64_t ldy, Operand x, Operand w, const void* z, int64_t ldz,
+                      int64_t rows, int64_t n, int64_t k, int32_t act, void* dx, void* dw, void* db,
+                      bool db_f32, const BackPlan& p, char* ws, cudaStream_t st) {
+  Operand dz{dy, n, rows, ldy};
+  if (p.make_dz || p.sums) {
+    T* dzp = p.make_dz ? reinterpret_cast<T*>(ws + p.dz) : nullptr;
+    float* part = p.sums ? reinterpret_cast<float*>(ws + p.part) : nullptr;
+    const int64_t ldd = round_up(n, 8), blocks = cdiv(rows, DZ_ROWS);
+    {
+      ProfScope ps_("k_lin_dz", st);
+      k_lin_dz<T><<<dim3((unsigned)blocks, (unsigned)cdiv(n, 256)), 256, 0, st>>>(
+          static_cast<const T*>(dy), ldy, static_cast<const T*>(z), ldz, act, rows, n, dzp, ldd, part,
+          aligned_rows(dy, ldy, 2, 16), aligned_rows(z, ldz, 2, 16));
+    }
+    count_launch();
+    MPQ_TRY(check_launch("k_lin_dz"));
+    if (p.sums) {
+      ProfScope ps_("k_lin_colsum", st);
+      if (db_f32)
+        k_lin_colsum<float><<<(unsigned)cdiv(n, 32), 256, 0, st>>>(part, blocks, n, static_cast<float*>(db));
+      else
+        k_lin_colsum<T><<<(unsigned)cdiv(n, 32), 256, 0, st>>>(part, blocks, n, static_cast<T*>(db));
+      count_launch();
+      MPQ_TRY(check_launch("k_lin_colsum"));
+    }
+    if (p.make_dz) dz = Operand{dzp, n, rows, ldd};
+  }
+  if (p.pack_x) MPQ_TRY(pack(&x, ws + p.x, st));
+  if (p.pack_w) MPQ_TRY(pack(&w, ws + p.w, st));
+  LinOut o{};
+  if (dx) {  // dx[rows x k] = dz[rows x n] W[n x k]: W has the output's columns contiguous
+    o.out = dx;
+    o.ldo = k;
+    o.rows = (int)rows;
+    o.cols = (int)k;
+    o.out_vec = aligned_rows(dx, k, 2, 16);
+    MPQ_TRY((lin_product<T, T, false, true>(dz, w, n, o, st, "k_linear_dx")));
+  }
+  if (dw) {  // dW[n x k] = dz^T x: both have their output index contiguous
+    o.out = dw;
+    o.ldo = k;
+    o.rows = (int)n;
+    o.cols = (int)k;
+    o.out_vec = aligned_rows(dw, k, 2, 16);
+    MPQ_TRY((lin_product<T, T, true, true>(dz, x, rows, o, st, "k_linear_dw")));
+  }
+  return MPQ_OK;
+}
+
+}  // namespace
+}  // namespace mpq
+
+using namespace mpq;
+
+extern "C" int64_t mpq_linear_workspace_bytes(const void* x, int64_t ldx, const void* weight, int64_t ldw,
+                                              int64_t rows, int64_t n, int64_t k) {
+  if (rows < 1 || n < 1 || k < 1) return 0;
+  return (tma_ok(x, k, rows, ldx) ? 0 : packed_bytes(k, rows)) + (tma_ok(weight, k, n, ldw) ? 0 : packed_bytes(k, n));
+}
+
+extern "C" mpq_status mpq_linear(const void* x, int64_t ldx, const void* weight, int64_t ldw, int64_t rows,
+                                 int64_t n, int64_t k, int32_t dtype, const void* bias, int32_t bias_dtype,
+                                 int32_t act, const void* residual, int64_t ldr, void* preact, void* y,
+                                 int32_t y_dtype, void* workspace, int64_t workspace_bytes, mpq_stream_t stream) {
+  MPQ_TRY(check_dims("linear", rows, n, k, dtype, act));
+  if (y_dtype != dtype && y_dtype != MPQ_F32)
+    return fail(MPQ_ERR_INVALID_ARG, "linear: the output must have the operands' type or fp32");
+  if (bias && bias_dtype != dtype && bias_dtype != MPQ_F32)
+    return fail(MPQ_ERR_INVALID_ARG, "linear: the bias must have the operands' type or fp32");
+  if (rows == 0) return MPQ_OK;
+  if (!x || !weight || !y) return fail(MPQ_ERR_INVALID_ARG, "linear: missing buffer");
+  const int64_t need = mpq_linear_workspace_bytes(x, ldx, weight, ldw, rows, n, k);
+  if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
+    return fail(MPQ_ERR_INVALID_ARG, "linear: needs " + std::to_string(need) +
+                                         " bytes of workspace on a 256-byte boundary");
+  LinOut o{};
+  const int64_t os = dtype_size(y_dtype);
+  o.bias = bias;
+  o.residual = residual;
+  o.preact = preact;
+  o.out = y;
+  o.ldr = ldr;
+  o.ldo = n;
+  o.rows = (int)rows;
+  o.cols = (int)n;
+  o.act = act;
+  o.bias_f32 = bias_dtype == MPQ_F32;
+  o.bias_vec = ((uintptr_t)bias & 15) == 0;
+  o.res_vec = aligned_rows(residual, ldr, os, 16);
+  o.out_vec = aligned_rows(y, n, os, 16) && aligned_rows(preact, n, 2, 16);
+  const Operand xo{x, k, rows, ldx}, wo{weight, k, n, ldw};
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == MPQ_BF16)
+    return y_dtype == MPQ_F32 ? linear_fwd<__nv_bfloat16, float>(xo, wo, o, ws, st)
+                              : linear_fwd<__nv_bfloat16, __nv_bfloat16>(xo, wo, o, ws, st);
+  return y_dtype == MPQ_F32 ? linear_fwd<__half, float>(xo, wo, o, ws, st)
+                            : linear_fwd<__half, __half>(xo, wo, o, ws, st);
+}
+
+extern "C" int64_t mpq_linear_backward_workspace_bytes(const void* dy, int64_t ldy, const void* x, int64_t ldx,
+                                                       const void* weight, int64_t ldw, int64_t rows, int64_t n,
+                                                       int64_t k, int32_t act, int32_t need_dx,
+                                                       int32_t need_dweight, int32_t need_dbias) {
+  if (rows < 1 || n < 1 || k < 1) return 0;
+  return back_plan(dy, ldy, x, ldx, weight, ldw, rows, n, k, act, need_dx != 0, need_dweight != 0,
+                   need_dbias != 0).total;
+}
+
+extern "C" mpq_status mpq_linear_backward(const void* dy, int64_t ldy, const void* x, int64_t ldx,
+                                          const void* weight, int64_t ldw, const void* preact, int64_t ldz,
+                                          int64_t rows, int64_t n, int64_t k, int32_t dtype, int32_t act,
+                                          void* dx, void* dweight, void* dbias, int32_t dbias_dtype,
+                                          void* workspace, int64_t workspace_bytes, mpq_stream_t stream) {
+  MPQ_TRY(check_dims("linear_backward", rows, n, k, dtype, act));
+  if (dbias && dbias_dtype != dtype && dbias_dtype != MPQ_F32)
+    return fail(MPQ_ERR_INVALID_ARG, "linear_backward: dbias must have the operands' type or fp32");
+  cudaStream_t st = (cudaStream_t)stream;
+  if (rows == 0) {  // nothing to sum: the parameters' gradients are zero
+    if (dweight) MPQ_CUDA(cudaMemsetAsync(dweight, 0, (size_t)(n * k * 2), st));
+    if (dbias) MPQ_CUDA(cudaMemsetAsync(dbias, 0, (size_t)(n * dtype_size(dbias_dtype)), st));
+    return MPQ_OK;
+  }
+  if (!dy || (dweight && !x) || (dx && !weight) || (act != MPQ_ACT_NONE && !preact))
+    return fail(MPQ_ERR_INVALID_ARG, "linear_backward: missing buffer");
+  const BackPlan p = back_plan(dy, ldy, x, ldx, weight, ldw, rows, n, k, act, dx != nullptr, dweight != nullptr,
+                               dbias != nullptr);
+  if (p.total > 0 && (!workspace || workspace_bytes < p.total || ((uintptr_t)workspace & 255)))
+    return fail(MPQ_ERR_INVALID_ARG, "linear_backward: needs " + std::to_string(p.total) +
+                                         " bytes of workspace on a 256-byte boundary");
+  const Operand xo{x, k, rows, ldx}, wo{weight, k, n, ldw};
+  char* ws = static_cast<char*>(workspace);
+  const bool f32 = dbias_dtype == MPQ_F32;
+  if (dtype == MPQ_BF16)
+    return linear_bwd<__nv_bfloat16>(dy, ldy, xo, wo, preact, ldz, rows, n, k, act, dx, dweight, dbias, f32, p, ws, st);
+  return linear_bwd<__half>(dy, ldy, xo, wo, preact, ldz, rows, n, k, act, dx, dweight, dbias, f32, p, ws, st);
+}
+
+extern "C" mpq_status mpq_ops_status(mpq_stream_t stream) {
+  cudaStream_t st = (cudaStream_t)stream;
+  int word = 0;
+  MPQ_CUDA(cudaMemcpyFromSymbolAsync(&word, g_lin_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st));
+  MPQ_CUDA(cudaStreamSynchronize(st));
+  if (!word) return MPQ_OK;
+  static const int zero = 0;
+  MPQ_CUDA(cudaMemcpyToSymbolAsync(g_lin_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st));
+  MPQ_CUDA(cudaStreamSynchronize(st));
+  return fail(MPQ_ERR_TIMEOUT, "a bounded wait of a linear kernel ran out");
+}
