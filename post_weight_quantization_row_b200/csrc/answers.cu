@@ -23,7 +23,6 @@
 
 #include "f32x2.cuh"
 #include "layer_ops.cuh"
-#include "tc_ptx.cuh"
 
 namespace mpq {
 namespace {
@@ -39,28 +38,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
-}
-
-// 8 elements as they lie in memory
-template <typename T>
-struct Raw8 {
-  uint4 q[sizeof(T) / 2];
-};
-template <typename T>
-__device__ __forceinline__ void decode(const Raw8<T>& r, float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const uint32_t w[8] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w, r.q[1].x, r.q[1].y, r.q[1].z, r.q[1].w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
-  } else {
-    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2(w[i], static_cast<const T*>(nullptr));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
 }
 
 // A row cut into vectors of 8 columns that start on 16-byte boundaries:
@@ -197,11 +174,6 @@ __device__ __forceinline__ void sync_row() {
   } else {
     __syncthreads();
   }
-}
-__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tcx::map_to_rank(tcx::smem_u32(p), (uint32_t)rank)) : "memory");
-  return v;
 }
 __device__ __forceinline__ uint64_t ld_cluster64(const uint64_t* p, int rank) {
   uint64_t v;

@@ -1,25 +1,29 @@
 // layer_norm: y = (x - mean) rstd w + b per row, and its backward pass with
 // the reduction of the parameters' gradients.
 //
-// Both are bound by HBM: the forward pass reads x and writes y, the backward
-// pass reads x and dy and writes dx.  A row is held in the registers of a
-// group of G threads (G = 4 .. 1024 by its width, 8 consecutive elements per
-// thread and vector), so it is read once: the mean, then the variance around
-// it, then the output.  The backward pass adds dw and db on the way: every
-// block walks rows with a fixed stride and each of its threads keeps the same
-// columns, so the sums stay in registers (in shared memory for wide rows) and
-// leave the block once, as one partial row per block; a second kernel adds
-// the partial rows in a fixed order.
+// Both are bound by HBM, and next by the issue of instructions: a bf16 element
+// of 2 bytes leaves about 18 issue slots of a lane at the copy rate, so the
+// arithmetic runs on packed pairs (f32x2) and decodes each element once.  A
+// row is held in the registers of a group of G threads, NV vectors of 8
+// elements each, so it is read once: the mean, then the variance around it,
+// then the output.  The backward pass adds dw and db on the way: every block
+// walks rows with a fixed stride and each of its threads keeps the same
+// columns, so the sums stay in registers and leave the block once, as one
+// partial row per block; a second kernel adds the partial rows in a fixed
+// order.
 #include <algorithm>
+#include <type_traits>
 
+#include "f32x2.cuh"
 #include "layer_ops.cuh"
 
 namespace mpq {
 namespace {
 
-constexpr int LN_BACK_BLOCKS = 296;        // partial rows of dw and db at most
+constexpr int LN_BACK_BLOCKS = 1184;       // partial rows of dw and db at most
 constexpr int64_t LN_REG_MAX = 32768;      // widest row held in registers (forward)
-constexpr int64_t LN_BACK_MAX = 16384;     // and in the one-pass backward kernel
+constexpr int LN_PART = 8192;              // columns per CTA of the backward kernel
+constexpr int64_t LN_BACK_MAX = 4 * LN_PART;  // widest row of a cluster of them
 constexpr int LN_COL_ROWS = 64;            // rows per partial of the wide rows' column sums
 
 // Sums over a group of G threads (a power of two): shuffles within a warp,
@@ -37,18 +41,24 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int G, float* scratch, 
   if (G > 32) {
     float* s = scratch + buf * (32 * N);
     buf ^= 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = G >> 5;
-    if (lane == 0) {
+    const int nw = G >> 5;  // 2, 4, .. 32 warps
+    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) s[warp * N + i] = v[i];
+      for (int i = 0; i < N; ++i) s[i * 32 + (threadIdx.x >> 5)] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane < nw ? s[lane * N + i] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int i = 0; i < N; ++i) {
+      if (nw == 2) {
+        v[i] = s[i * 32] + s[i * 32 + 1];
+      } else {
+        float t = 0.0f;
+        for (int w = 0; w < nw; w += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(s + i * 32 + w);
+          t += (q.x + q.y) + (q.z + q.w);
+        }
+        v[i] = t;
+      }
     }
   }
 }
@@ -59,64 +69,186 @@ struct LnArgs {
   const void* w;
   const void* b;
   bool p_f32, x_vec, p_vec, o_vec;
-  int G;
+  int G, C;
 };
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(1024)
+// How the parameters come: none, both in T, both in fp32 (rows and parameters
+// then start on 16-byte boundaries and hold whole vectors of 8), or ANY: the
+// general form, element by element.
+enum { PM_NONE = 0, PM_T = 1, PM_F32 = 2, PM_ANY = 3 };
+
+// The column of element i of vector j of a thread t of G: 8 neighbours, one
+// or two wide accesses, or for PM_ANY single elements G apart, so that a
+// warp's accesses still cover neighbouring ones.
+template <int PM>
+__device__ __forceinline__ int ln_col(int t, int G, int j, int i) {
+  return PM != PM_ANY ? (t + j * G) * 8 + i : (j * 8 + i) * G + t;
+}
+template <int PM, typename T>
+__device__ __forceinline__ Raw8<T> ln_load(const T* row, int n, int t, int G, int j) {
+  Raw8<T> r;
+  if (PM != PM_ANY) {
+    const int c = (t + j * G) * 8;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+      r.q[i] = c < n ? reinterpret_cast<const uint4*>(row + c)[i] : make_uint4(0, 0, 0, 0);
+    return r;
+  }
+  T e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = ln_col<PM>(t, G, j, i) < n ? row[ln_col<PM>(t, G, j, i)] : from_f<T>(0.0f);
+  memcpy(&r, e, sizeof(r));
+  return r;
+}
+template <int PM, typename T>
+__device__ __forceinline__ void ln_store(T* row, const float (&v)[8], int n, int t, int G, int j) {
+  if (PM != PM_ANY) {
+    const int c = (t + j * G) * 8;
+    if (c < n) store_vec<8>(row + c, v, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (ln_col<PM>(t, G, j, i) < n) row[ln_col<PM>(t, G, j, i)] = from_f<T>(v[i]);
+  }
+}
+template <int PM, typename T>
+__device__ __forceinline__ void ln_param(const LnArgs& a, const void* p, float dflt, int t, int j, float (&w)[8]) {
+  const int n = (int)a.n;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = dflt;
+  if (PM == PM_NONE) return;
+  if (PM != PM_ANY) {
+    const int c = (t + j * a.G) * 8;
+    if (c >= n) return;
+    if (PM == PM_T) load_vec<8>(static_cast<const T*>(p) + c, w, true);
+    else load_vec<8>(static_cast<const float*>(p) + c, w, true);
+    return;
+  }
+  if (!p) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = ln_col<PM>(t, a.G, j, i);
+    if (c < n) w[i] = a.p_f32 ? static_cast<const float*>(p)[c] : to_f(static_cast<const T*>(p)[c]);
+  }
+}
+
+// 8 elements as 4 packed pairs
+struct F8 {
+  uint64_t p[4];
+};
+template <typename T>
+__device__ __forceinline__ F8 pairs(const Raw8<T>& r) {
+  float v[8];
+  decode<T>(r, v);
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+  return f;
+}
+__device__ __forceinline__ F8 pairs(const float (&v)[8]) {
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+  return f;
+}
+__device__ __forceinline__ void unpairs(const F8& f, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(f.p[i], v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ float f2_sum(uint64_t a) {
+  float x, y;
+  f2_unpack(a, x, y);
+  return x + y;
+}
+// NR rows at a time per group (narrow rows): more loads in flight, and the
+// parameters are read once for NR rows.
+template <typename T, int NV, int NR, int PM>
+__global__ void __launch_bounds__(NV * NR >= 8 ? 256 : 1024)
     k_ln_fwd(const __grid_constant__ LnArgs a, float eps, T* __restrict__ y, float* __restrict__ mean_out,
              float* __restrict__ rstd_out) {
-  __shared__ float scratch[2 * 32];
+  __shared__ __align__(16) float scratch[2 * 32 * NR];
   int buf = 0;
   const int t = threadIdx.x & (a.G - 1);
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / a.G) + threadIdx.x / a.G;
-  const bool live = row < a.rows;
-  const T* xr = static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx;
+  const int64_t row0 = ((int64_t)blockIdx.x * (blockDim.x / a.G) + threadIdx.x / a.G) * NR;
   const int n = (int)a.n;
-  float v[NV][8];
-  float s[1] = {0.0f};
+  const float inv_n = 1.0f / (float)n;
+  F8 v[NR][NV];
+  {
+    Raw8<T> x[NR][NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (t + j * a.G) * 8;
-    if (live && c < n) load_edge<8>(xr + c, v[j], n - c, a.x_vec);
-    else {
+    for (int r = 0; r < NR; ++r) {
+      const T* xr = static_cast<const T*>(a.x) + (row0 + r < a.rows ? row0 + r : 0) * a.ldx;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+      for (int j = 0; j < NV; ++j) x[r][j] = ln_load<PM, T>(xr, n, t, a.G, j);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] += v[j][i];
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[r][j] = pairs<T>(x[r][j]);
   }
-  group_sum<1>(s, a.G, scratch, buf);
-  const float mean = s[0] / (float)n;
-  float q[1] = {0.0f};
+  float mean[NR], rstd[NR];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (t + j * a.G) * 8;
+  for (int r = 0; r < NR; ++r) {
+    uint64_t s0 = 0ull, s1 = 0ull;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[j][i] -= mean;
-      if (c + i < n) q[0] = fmaf(v[j][i], v[j][i], q[0]);
+    for (int j = 0; j < NV; ++j) {
+      s0 = f2_add(s0, f2_add(v[r][j].p[0], v[r][j].p[1]));
+      s1 = f2_add(s1, f2_add(v[r][j].p[2], v[r][j].p[3]));
+    }
+    mean[r] = f2_sum(f2_add(s0, s1));
+  }
+  group_sum<NR>(mean, a.G, scratch, buf);
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    mean[r] *= inv_n;
+    const uint64_t m2 = f2_pack(-mean[r], -mean[r]);
+    uint64_t s0 = 0ull, s1 = 0ull;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[r][j].p[i] = f2_add(v[r][j].p[i], m2);
+      if (PM == PM_ANY) {  // columns that do not exist hold -mean: out
+        float e[8];
+        unpairs(v[r][j], e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (ln_col<PM>(t, a.G, j, i) >= n) e[i] = 0.0f;
+        v[r][j] = pairs(e);
+      }
+      if (PM == PM_ANY || (t + j * a.G) * 8 < n) {
+        s0 = f2_fma(v[r][j].p[0], v[r][j].p[0], s0);
+        s1 = f2_fma(v[r][j].p[1], v[r][j].p[1], s1);
+        s0 = f2_fma(v[r][j].p[2], v[r][j].p[2], s0);
+        s1 = f2_fma(v[r][j].p[3], v[r][j].p[3], s1);
+      }
+    }
+    rstd[r] = f2_sum(f2_add(s0, s1));
+  }
+  group_sum<NR>(rstd, a.G, scratch, buf);
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    rstd[r] = 1.0f / sqrtf(fmaf(rstd[r], inv_n, eps));
+    if (t == 0 && row0 + r < a.rows) {
+      if (mean_out) mean_out[row0 + r] = mean[r];
+      if (rstd_out) rstd_out[row0 + r] = rstd[r];
     }
   }
-  group_sum<1>(q, a.G, scratch, buf);
-  if (!live) return;
-  const float rstd = 1.0f / sqrtf(q[0] / (float)n + eps);
-  if (t == 0) {
-    if (mean_out) mean_out[row] = mean;
-    if (rstd_out) rstd_out[row] = rstd;
-  }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (t + j * a.G) * 8;
-    if (c >= n) break;
     float w[8], b[8];
+    ln_param<PM, T>(a, a.w, 1.0f, t, j, w);
+    ln_param<PM, T>(a, a.b, 0.0f, t, j, b);
+    const F8 w2 = pairs(w), b2 = pairs(b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { w[i] = 1.0f; b[i] = 0.0f; }
-    if (a.w) load_param<8, T>(a.w, a.p_f32, c, w, n - c, a.p_vec);
-    if (a.b) load_param<8, T>(a.b, a.p_f32, c, b, n - c, a.p_vec);
+    for (int r = 0; r < NR; ++r) {
+      if (row0 + r >= a.rows) break;
+      const uint64_t r2 = f2_pack(rstd[r], rstd[r]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = fmaf(v[j][i] * rstd, w[i], b[i]);
-    store_edge<8>(y + row * a.n + c, w, n - c, a.o_vec);
+      for (int i = 0; i < 4; ++i) v[r][j].p[i] = f2_fma(f2_mul(v[r][j].p[i], r2), w2.p[i], b2.p[i]);
+      float o[8];
+      unpairs(v[r][j], o);
+      ln_store<PM, T>(y + (row0 + r) * a.n, o, n, t, a.G, j);
+    }
   }
 }
 
@@ -126,7 +258,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024)
     k_ln_fwd_wide(const __grid_constant__ LnArgs a, float eps, T* __restrict__ y, float* __restrict__ mean_out,
                   float* __restrict__ rstd_out) {
-  __shared__ float scratch[2 * 32];
+  __shared__ __align__(16) float scratch[2 * 32];
   int buf = 0;
   const int64_t row = blockIdx.x;
   const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
@@ -168,109 +300,138 @@ __global__ void __launch_bounds__(1024)
 }
 
 // --------------------------------------------------------------- backward --
-enum { ACC_NONE = 0, ACC_REG = 1, ACC_SMEM = 2 };
-
-// dx of rows row0, row0 + step, ... and, per block, the column sums of dy xh
-// and dy over those rows.  The next row's loads are issued before this row's
-// sums are joined.
-template <typename T, int NV, int ACC>
-__global__ void __launch_bounds__(1024)
-    k_ln_bwd(const __grid_constant__ LnArgs a, const T* __restrict__ dy, int64_t ldy, bool y_vec,
+// dx of a row at a time per group, walking the rows with a fixed stride, and
+// (SUMS) per block the column sums of dy xh and dy over its rows.  The next
+// row's loads are issued before this row's sums are joined.  CL: a cluster of
+// CTAs shares the rows, LN_PART columns each; their sums meet over distributed
+// shared memory.
+template <typename T, int NV, int PM, bool SUMS, bool CL>
+__global__ void __launch_bounds__(NV == 1 ? 128 : 512)
+    k_ln_bwd(const __grid_constant__ LnArgs a, const T* __restrict__ dy, int64_t ldy,
              const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
              float* __restrict__ part) {
-  __shared__ float scratch[2 * 64];
-  extern __shared__ float accs[];  // ACC_SMEM: dw[n8], db[n8]; ACC_REG with several groups: the join
+  __shared__ __align__(16) float scratch[2 * 64];
+  __shared__ float meet[2][2];     // CL: this CTA's sums, alternating between rows
+  extern __shared__ float join[];  // several groups: dw[n], db[n]
   int buf = 0;
   const int t = threadIdx.x & (a.G - 1), groups = blockDim.x / a.G;
-  const int n = (int)a.n;
-  const float inv_n = 1.0f / (float)n;
-  constexpr int NA = ACC == ACC_REG ? NV : 1;
-  float dw[NA][8], db[NA][8];
+  const int C = CL ? a.C : 1, rank = CL ? (int)tcx::cluster_ctarank() : 0;
+  const int c0 = CL ? rank * LN_PART : 0;
+  const int n = CL ? min(LN_PART, (int)a.n - c0) : (int)a.n;  // this CTA's columns
+  const int64_t block = blockIdx.x / C, nblocks = gridDim.x / C;
+  const float inv_n = 1.0f / (float)a.n;
+  LnArgs pa = a;  // the parameters of these columns
+  pa.n = n;
+  if (CL && a.w) pa.w = static_cast<const char*>(a.w) + (int64_t)c0 * (a.p_f32 ? 4 : (int)sizeof(T));
+  F8 dw2[NV], db2[NV];
 #pragma unroll
-  for (int j = 0; j < NA; ++j)
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { dw[j][i] = 0.0f; db[j][i] = 0.0f; }
-  const int n8 = (n + 7) / 8 * 8;
-  if (ACC == ACC_SMEM) {  // each thread clears and later adds to its own columns only
-    for (int c = t * 8; c < n8; c += a.G * 8)
+    for (int i = 0; i < 4; ++i) dw2[j].p[i] = db2[j].p[i] = 0ull;
+  const int64_t step = nblocks * groups;
+  int64_t row = block * groups + threadIdx.x / a.G;
+  Raw8<T> xs[NV], ds[NV];
+  float m = 0.0f, r = 0.0f;
+  const auto fetch = [&](int64_t at) {  // (rows that do not exist: zeros)
+    const bool live = at < a.rows;
+    const T* xr = static_cast<const T*>(a.x) + (live ? at : 0) * a.ldx + c0;
+    const T* yr = dy + (live ? at : 0) * ldy + c0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) { accs[c + i] = 0.0f; accs[n8 + c + i] = 0.0f; }
-  }
-  const int64_t step = (int64_t)gridDim.x * groups;
+    for (int j = 0; j < NV; ++j) {
+      xs[j] = ln_load<PM, T>(xr, live ? n : 0, t, a.G, j);
+      ds[j] = ln_load<PM, T>(yr, live ? n : 0, t, a.G, j);
+    }
+    m = live ? mean[at] : 0.0f;
+    r = live ? rstd[at] : 0.0f;
+  };
+  fetch(row);
   // every thread of the block takes the same number of turns (group_sum)
-  for (int64_t base = (int64_t)blockIdx.x * groups; base < a.rows; base += step) {
-    const int64_t row = base + threadIdx.x / a.G;
-    const bool live = row < a.rows;
-    const T* xr = static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx;
-    const T* yr = dy + (live ? row : 0) * ldy;
-    float xh[NV][8], g[NV][8];
+  for (int64_t base = block * groups; base < a.rows; base += step, row += step) {
+    F8 xh[NV], g[NV];
+    const uint64_t m2 = f2_pack(-m, -m), r2 = f2_pack(r, r);
+    const float rr = r;
+    uint64_t t0 = 0ull, t1 = 0ull;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (t + j * a.G) * 8;
-      if (live && c < n) {
-        load_edge<8>(xr + c, xh[j], n - c, a.x_vec);
-        load_edge<8>(yr + c, g[j], n - c, y_vec);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) { xh[j][i] = 0.0f; g[j][i] = 0.0f; }
-      }
-    }
-    const float m = live ? mean[row] : 0.0f, r = live ? rstd[row] : 0.0f;
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (t + j * a.G) * 8;
       float w[8];
+      ln_param<PM, T>(pa, pa.w, 1.0f, t, j, w);
+      const F8 w2 = pairs(w);
+      xh[j] = pairs<T>(xs[j]);
+      g[j] = pairs<T>(ds[j]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-      if (a.w && c < n) load_param<8, T>(a.w, a.p_f32, c, w, n - c, a.p_vec);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xh[j][i] = (live && c + i < n) ? (xh[j][i] - m) * r : 0.0f;
-        const float d = g[j][i];
-        if (ACC == ACC_REG) {
-          dw[ACC == ACC_REG ? j : 0][i] = fmaf(d, xh[j][i], dw[ACC == ACC_REG ? j : 0][i]);
-          db[ACC == ACC_REG ? j : 0][i] += d;
+      for (int i = 0; i < 4; ++i) {
+        // (columns that do not exist: dy = 0 there, and xh is finite)
+        xh[j].p[i] = f2_mul(f2_add(xh[j].p[i], m2), r2);
+        if (SUMS) {
+          dw2[j].p[i] = f2_fma(g[j].p[i], xh[j].p[i], dw2[j].p[i]);
+          db2[j].p[i] = f2_add(g[j].p[i], db2[j].p[i]);
         }
-        if (ACC == ACC_SMEM && c < n) {
-          accs[c + i] = fmaf(d, xh[j][i], accs[c + i]);
-          accs[n8 + c + i] += d;
-        }
-        g[j][i] = d * w[i];
-        s[0] += g[j][i];
-        s[1] = fmaf(g[j][i], xh[j][i], s[1]);
+        g[j].p[i] = f2_mul(g[j].p[i], w2.p[i]);
+        t0 = f2_add(t0, g[j].p[i]);
+        t1 = f2_fma(g[j].p[i], xh[j].p[i], t1);
       }
     }
+    fetch(row + step);
     if (dx) {
+      float s[2] = {f2_sum(t0), f2_sum(t1)};
       group_sum<2>(s, a.G, scratch, buf);
-      const float s0 = s[0] * inv_n, s1 = s[1] * inv_n;
-      if (live) {
+      if (CL) {
+        if (threadIdx.x == 0) {
+          meet[buf][0] = s[0];
+          meet[buf][1] = s[1];
+        }
+        __syncwarp();
+        tcx::cluster_sync();
+        s[0] = s[1] = 0.0f;
+        for (int q = 0; q < C; ++q) {
+          s[0] += ld_cluster(&meet[buf][0], q);
+          s[1] += ld_cluster(&meet[buf][1], q);
+        }
+      }
+      if (row < a.rows) {
+        const uint64_t s0 = f2_pack(-s[0] * inv_n, -s[0] * inv_n), s1 = f2_pack(-s[1] * inv_n, -s[1] * inv_n);
+        const uint64_t q2 = f2_pack(rr, rr);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          const int c = (t + j * a.G) * 8;
-          if (c >= n) break;
+          float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[j][i] = r * (g[j][i] - fmaf(xh[j][i], s1, s0));
-          store_edge<8>(dx + row * a.n + c, g[j], n - c, a.o_vec);
+          for (int i = 0; i < 4; ++i)
+            g[j].p[i] = f2_mul(q2, f2_fma(xh[j].p[i], s1, f2_add(g[j].p[i], s0)));
+          unpairs(g[j], o);
+          ln_store<PM, T>(dx + row * a.n + c0, o, n, t, a.G, j);
         }
       }
     }
   }
-  if (ACC == ACC_NONE) return;
-  float* pw = part + (int64_t)blockIdx.x * 2 * n;
-  float* pb = pw + n;
-  if (ACC == ACC_SMEM) {
-    for (int c = t * 8; c < n; c += a.G * 8)
-      for (int i = 0; i < 8 && c + i < n; ++i) { pw[c + i] = accs[c + i]; pb[c + i] = accs[n8 + c + i]; }
-    return;
+  if (CL) {
+    __syncwarp();
+    tcx::cluster_sync();  // no peer still reads this CTA's sums
   }
+  if (!SUMS) return;
+  float dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    unpairs(dw2[j], dw[j]);
+    unpairs(db2[j], db[j]);
+  }
+  float* pw = part + block * 2 * a.n + c0;
+  float* pb = pw + a.n;
   if (groups == 1) {
 #pragma unroll
-    for (int j = 0; j < NA; ++j) {
-      const int c = (t + j * a.G) * 8;
+    for (int j = 0; j < NV; ++j) {
+      if (PM != PM_ANY) {
+        const int c = (t + j * a.G) * 8;
+        if (c < n) {
+          store_vec<8>(pw + c, dw[j], true);
+          store_vec<8>(pb + c, db[j], true);
+        }
+        continue;
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < n) { pw[c + i] = dw[j][i]; pb[c + i] = db[j][i]; }
+      for (int i = 0; i < 8; ++i) {
+        const int c = ln_col<PM>(t, a.G, j, i);
+        if (c < n) { pw[c] = dw[j][i]; pb[c] = db[j][i]; }
+      }
     }
     return;
   }
@@ -278,19 +439,19 @@ __global__ void __launch_bounds__(1024)
   for (int q = 0; q < groups; ++q) {
     if (threadIdx.x / a.G == q) {
 #pragma unroll
-      for (int j = 0; j < NA; ++j) {
-        const int c = (t + j * a.G) * 8;
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c + i < n) {
-            accs[c + i] = (q ? accs[c + i] : 0.0f) + dw[j][i];
-            accs[n8 + c + i] = (q ? accs[n8 + c + i] : 0.0f) + db[j][i];
+        for (int i = 0; i < 8; ++i) {
+          const int c = ln_col<PM>(t, a.G, j, i);
+          if (c < n) {
+            join[c] = (q ? join[c] : 0.0f) + dw[j][i];
+            join[n + c] = (q ? join[n + c] : 0.0f) + db[j][i];
           }
-      }
+        }
     }
     __syncthreads();
   }
-  for (int c = threadIdx.x; c < n; c += blockDim.x) { pw[c] = accs[c]; pb[c] = accs[n8 + c]; }
+  for (int c = threadIdx.x; c < n; c += blockDim.x) { pw[c] = join[c]; pb[c] = join[n + c]; }
 }
 
 // Rows too wide for the kernel above: dx in two passes over the row, and the
@@ -299,7 +460,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024)
     k_ln_dx_wide(const __grid_constant__ LnArgs a, const T* __restrict__ dy, int64_t ldy, bool y_vec,
                  const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx) {
-  __shared__ float scratch[2 * 64];
+  __shared__ __align__(16) float scratch[2 * 64];
   int buf = 0;
   const int64_t row = blockIdx.x;
   const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
@@ -373,37 +534,39 @@ __global__ void __launch_bounds__(256)
 
 // dw and db from the blocks' partial rows, in a fixed order.
 template <typename O>
-__global__ void __launch_bounds__(512)
-    k_ln_dparam(const float* __restrict__ part, int64_t blocks, int64_t n, O* __restrict__ dw, O* __restrict__ db) {
-  __shared__ float red[2][16][32];
+__global__ void __launch_bounds__(1024)
+    k_ln_dparam(const float* __restrict__ part, int blocks, int64_t n, O* __restrict__ dw, O* __restrict__ db) {
+  __shared__ float red[2][32][33];
   const int cl = threadIdx.x & 31, bl = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + cl;
   float s = 0.0f, t = 0.0f;
-  if (c < n)
-    for (int64_t b = bl; b < blocks; b += 16) {
-      s += part[(2 * b) * n + c];
-      t += part[(2 * b + 1) * n + c];
+  if (c < n) {
+#pragma unroll 8
+    for (int b = bl; b < blocks; b += 32) {
+      s += part[(2 * (int64_t)b) * n + c];
+      t += part[(2 * (int64_t)b + 1) * n + c];
     }
+  }
   red[0][bl][cl] = s;
   red[1][bl][cl] = t;
   __syncthreads();
   if (bl < 2 && c < n) {
     float u = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) u += red[bl][i][cl];
+    for (int i = 0; i < 32; ++i) u += red[bl][i][cl];
     O* out = bl ? db : dw;
     if (out) out[c] = from_f<O>(u);
   }
 }
 
-// Threads per row for nv vectors of 8 per thread
-int group_threads(int64_t n, int nv) {
-  int g = 4;
+// The smallest group (a power of two) that holds n columns in nv vectors a
+// thread, between lo and 1024 threads.
+int group_threads(int64_t n, int nv, int lo) {
+  int g = lo;
   while ((int64_t)g * nv * 8 < n) g *= 2;
   return g;
 }
-int fwd_vectors(int64_t n) { return n <= 8192 ? 1 : n <= 16384 ? 2 : 4; }
-int bwd_vectors(int64_t n) { return n <= 8192 ? 1 : 2; }
+
 mpq_status ln_check(const char* who, int64_t rows, int64_t n, int32_t dtype, const void* w, const void* b,
                     int32_t pd) {
   if (rows < 0 || rows > MAX_ROWS || n < 1 || n > (1 << 20))
@@ -414,33 +577,68 @@ mpq_status ln_check(const char* who, int64_t rows, int64_t n, int32_t dtype, con
   return MPQ_OK;
 }
 
+template <typename T, int PM>
+void ln_fwd_rows(LnArgs a, float e, T* y, float* mean, float* rstd, cudaStream_t st) {
+  const auto go = [&](auto kernel, int nv, int nr) {
+    a.G = group_threads(a.n, nv, 4);
+    const int block = a.G > 32 ? a.G : 128;  // a group of several warps is the whole block
+    kernel<<<(unsigned)cdiv(a.rows, (int64_t)(block / a.G) * nr), block, 0, st>>>(a, e, y, mean, rstd);
+  };
+  // One vector a thread where there are too few rows to fill the device with
+  // small groups; 4 otherwise: a row of 4096 then has one barrier between 4
+  // warps per sum, and 8 rows are at work on an SM.
+  const bool few = a.rows * cdiv(a.n, 1024) < 148 * 8;
+  if (few && a.n <= 8192) go(k_ln_fwd<T, 1, 1, PM>, 1, 1);
+  else if (a.n <= 256) go(k_ln_fwd<T, 1, 4, PM>, 1, 4);
+  else if (a.n <= 512) go(k_ln_fwd<T, 2, 2, PM>, 2, 2);
+  // (fp32 parameters weigh as much as four rows of 16-bit elements: 16384 x
+  // 4096 takes 55 us with two rows a group, 61 with one; with 16-bit
+  // parameters 8000 x 8192 takes 64 and 56)
+  else if (PM == PM_F32 && sizeof(T) == 2 && a.n <= 8192) go(k_ln_fwd<T, 4, 2, PM>, 4, 2);
+  else go(k_ln_fwd<T, 4, 1, PM>, 4, 1);
+}
 template <typename T>
-mpq_status ln_fwd(LnArgs a, double eps, void* y, float* mean, float* rstd, cudaStream_t st) {
+mpq_status ln_fwd(const LnArgs& a, double eps, void* y, float* mean, float* rstd, cudaStream_t st) {
   T* yo = static_cast<T*>(y);
   const float e = (float)eps;
   ProfScope ps_("k_layer_norm", st);
-  if (a.n > LN_REG_MAX) {
-    k_ln_fwd_wide<T><<<(unsigned)a.rows, 1024, 0, st>>>(a, e, yo, mean, rstd);
-  } else {
-    const int nv = fwd_vectors(a.n);
-    a.G = group_threads(a.n, nv);
-    const int block = std::max(a.G, 128);
-    const unsigned grid = (unsigned)cdiv(a.rows, block / a.G);
-    if (a.G > 32 && block != a.G) {  // a group of several warps is the whole block
-      const unsigned rows = (unsigned)a.rows;
-      k_ln_fwd<T, 1><<<rows, a.G, 0, st>>>(a, e, yo, mean, rstd);
-    } else if (nv == 1) {
-      k_ln_fwd<T, 1><<<grid, block, 0, st>>>(a, e, yo, mean, rstd);
-    } else if (nv == 2) {
-      k_ln_fwd<T, 2><<<grid, block, 0, st>>>(a, e, yo, mean, rstd);
-    } else {
-      k_ln_fwd<T, 4><<<grid, block, 0, st>>>(a, e, yo, mean, rstd);
-    }
-  }
+  if (a.n > LN_REG_MAX) k_ln_fwd_wide<T><<<(unsigned)a.rows, 1024, 0, st>>>(a, e, yo, mean, rstd);
+  else if (!a.x_vec || !a.p_vec || !a.o_vec || a.n % 8 || !a.w != !a.b) ln_fwd_rows<T, PM_ANY>(a, e, yo, mean, rstd, st);
+  else if (!a.w) ln_fwd_rows<T, PM_NONE>(a, e, yo, mean, rstd, st);
+  else if (a.p_f32) ln_fwd_rows<T, PM_F32>(a, e, yo, mean, rstd, st);
+  else ln_fwd_rows<T, PM_T>(a, e, yo, mean, rstd, st);
   count_launch();
   return check_launch("k_layer_norm");
 }
 
+template <typename T, int PM, bool SUMS>
+mpq_status ln_bwd_rows(LnArgs a, const T* dy, int64_t ldy, const float* mean, const float* rstd, T* dx, float* part,
+                       int64_t* blocks, cudaStream_t st) {
+  const auto go = [&](auto kernel, int nv) -> mpq_status {
+    a.C = (int)cdiv(a.n, LN_PART);
+    a.G = a.C > 1 ? LN_PART / 16 : group_threads(a.n, nv, 4);
+    const int block = a.G > 32 ? a.G : 128;
+    const int64_t groups = block / a.G;
+    *blocks = std::min<int64_t>(cdiv(a.rows, groups), 148 * std::max(1, std::min(8, 512 / block)) / a.C);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(*blocks * a.C));
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = SUMS && groups > 1 ? (size_t)(2 * a.n * 4) : 0;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)a.C;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.C > 1 ? 1 : 0;
+    MPQ_CUDA(cudaLaunchKernelEx(&cfg, kernel, (const LnArgs)a, dy, ldy, mean, rstd, dx, part));
+    return MPQ_OK;
+  };
+  if (a.n <= 256) return go(k_ln_bwd<T, 1, PM, SUMS, false>, 1);
+  if (a.n <= LN_PART) return go(k_ln_bwd<T, 2, PM, SUMS, false>, 2);
+  return go(k_ln_bwd<T, 2, PM, SUMS, true>, 2);
+}
 template <typename T>
 mpq_status ln_bwd(LnArgs a, const void* dy, int64_t ldy, bool y_vec, const float* mean, const float* rstd,
                   void* dx, void* dw, void* db, float* part, cudaStream_t st) {
@@ -464,33 +662,24 @@ mpq_status ln_bwd(LnArgs a, const void* dy, int64_t ldy, bool y_vec, const float
       MPQ_TRY(check_launch("k_ln_cols_wide"));
     }
   } else {
-    const int nv = bwd_vectors(a.n);
-    a.G = group_threads(a.n, nv);
-    const int block = a.G < 256 ? (a.G > 32 ? a.G : 256) : a.G;
-    const int groups = block / a.G;
-    blocks = std::min<int64_t>(cdiv(a.rows, groups), LN_BACK_BLOCKS);
-    const int n8 = (int)round_up(a.n, 8);
     ProfScope ps_("k_ln_bwd", st);
-    if (!sums) {
-      const unsigned grid = (unsigned)std::min<int64_t>(cdiv(a.rows, groups), 148 * 8);
-      if (nv == 1) k_ln_bwd<T, 1, ACC_NONE><<<grid, block, 0, st>>>(a, dyp, ldy, y_vec, mean, rstd, dxp, nullptr);
-      else k_ln_bwd<T, 2, ACC_NONE><<<grid, block, 0, st>>>(a, dyp, ldy, y_vec, mean, rstd, dxp, nullptr);
-    } else if (nv == 1) {
-      const int smem = groups > 1 ? 2 * n8 * 4 : 0;
-      k_ln_bwd<T, 1, ACC_REG><<<(unsigned)blocks, block, smem, st>>>(a, dyp, ldy, y_vec, mean, rstd, dxp, part);
-    } else {
-      MPQ_CUDA(cudaFuncSetAttribute(k_ln_bwd<T, 2, ACC_SMEM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)(2 * LN_BACK_MAX * 4)));
-      k_ln_bwd<T, 2, ACC_SMEM><<<(unsigned)blocks, block, 2 * n8 * 4, st>>>(a, dyp, ldy, y_vec, mean, rstd, dxp, part);
-    }
+    const auto go = [&](auto pm) {
+      constexpr int PM = decltype(pm)::value;
+      return sums ? ln_bwd_rows<T, PM, true>(a, dyp, ldy, mean, rstd, dxp, part, &blocks, st)
+                  : ln_bwd_rows<T, PM, false>(a, dyp, ldy, mean, rstd, dxp, part, &blocks, st);
+    };
+    if (!a.x_vec || !y_vec || !a.p_vec || !a.o_vec || a.n % 8) MPQ_TRY(go(std::integral_constant<int, PM_ANY>{}));
+    else if (!a.w) MPQ_TRY(go(std::integral_constant<int, PM_NONE>{}));
+    else if (a.p_f32) MPQ_TRY(go(std::integral_constant<int, PM_F32>{}));
+    else MPQ_TRY(go(std::integral_constant<int, PM_T>{}));
     count_launch();
     MPQ_TRY(check_launch("k_ln_bwd"));
   }
   if (sums) {
     ProfScope ps_("k_ln_dparam", st);
     const unsigned grid = (unsigned)cdiv(a.n, 32);
-    if (a.p_f32) k_ln_dparam<float><<<grid, 512, 0, st>>>(part, blocks, a.n, static_cast<float*>(dw), static_cast<float*>(db));
-    else k_ln_dparam<T><<<grid, 512, 0, st>>>(part, blocks, a.n, static_cast<T*>(dw), static_cast<T*>(db));
+    if (a.p_f32) k_ln_dparam<float><<<grid, 1024, 0, st>>>(part, (int)blocks, a.n, static_cast<float*>(dw), static_cast<float*>(db));
+    else k_ln_dparam<T><<<grid, 1024, 0, st>>>(part, (int)blocks, a.n, static_cast<T*>(dw), static_cast<T*>(db));
     count_launch();
     return check_launch("k_ln_dparam");
   }

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "mpq_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace mpq {
 
@@ -127,10 +128,59 @@ __device__ __forceinline__ void store_param(void* p, bool f32, int64_t at, const
   else store_edge<W>(static_cast<T*>(p) + at, v, n, vec);
 }
 
+// 8 consecutive elements as they lie in memory: half the registers of floats
+// for 16-bit types.
+template <typename T>
+struct Raw8 {
+  uint4 q[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void decode(const Raw8<T>& r, float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t w[8] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w, r.q[1].x, r.q[1].y, r.q[1].z, r.q[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  } else {
+    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2(w[i], static_cast<const T*>(nullptr));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+// The first n of 8 elements (all for n >= 8, none for n <= 0), the others 0;
+// vec: the address is on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T* p, int n, bool vec) {
+  Raw8<T> r;
+  if (n >= 8 && vec) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.q[i] = reinterpret_cast<const uint4*>(p)[i];
+  } else {
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : from_f<T>(0.0f);
+    memcpy(&r, e, sizeof(r));
+  }
+  return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 ulp; 0 below 2^-126
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// a float at the same shared-memory place in CTA `rank` of the cluster
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];"
+               : "=f"(v)
+               : "r"(tcx::map_to_rank(tcx::smem_u32(p), (uint32_t)rank))
+               : "memory");
+  return v;
 }
 
 inline bool aligned_rows(const void* p, int64_t ld, int64_t elem, int64_t bytes) {

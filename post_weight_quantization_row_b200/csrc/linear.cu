@@ -24,7 +24,6 @@
 #include <mutex>
 
 #include "layer_ops.cuh"
-#include "tc_ptx.cuh"
 
 namespace mpq {
 namespace {

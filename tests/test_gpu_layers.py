@@ -250,17 +250,29 @@ def test_layer_norm_slices_missing_parameters_and_edges(mpq, n):
     wide = torch.randn(4, 3, n + 5, generator=g, device="cuda").to(BF)
     x = wide[..., 1:n + 1]
     y = mpq.layer_norm(x)
-    assert torch.equal(y, mpq.layer_norm(x.contiguous())) and y.shape == (4, 3, n)
+    # other layouts may take other orders of the same fp32 sums: both results are within 128 roundings of the
+    # magnitudes that go into them, so within twice that and one step of bf16 of each other
+    x64 = x.double()
+    y2, m2, r2 = mpq.layer_norm(x.contiguous(), stats=True)
+    scale = x64.abs().mean(-1, keepdim=True) * r2[..., None] + y2.double().abs()
+    within(y, y2.double(), 2 * half(BF) * y2.double().abs() + 256 * U * scale, "y")
+    assert y.shape == (4, 3, n) and m2.shape == (4, 3)
     one, zero = torch.ones(n, device="cuda"), torch.zeros(n, device="cuda")
     assert torch.equal(y, mpq.layer_norm(x, one, zero))
     y, mean, rstd = mpq.layer_norm(x, stats=True)
     dy = torch.randn(4, 3, n + 3, generator=g, device="cuda").to(BF)[..., 2:n + 2]
     a = mpq.layer_norm_backward(dy, x, mean, rstd, param_dtype=F32)
     c = mpq.layer_norm_backward(dy.contiguous(), x.contiguous(), mean, rstd, one)
-    for name in ("dx", "dweight", "dbias"):
-        assert torch.equal(a[name], c[name]), name
+    # other layouts may take other orders of the same fp32 sums: each is within 128 roundings of its magnitudes
+    # (12 rows, 64 levels and chains), so the two are within twice that, and one step of bf16 apart at most
+    xh, m = (x.double() - mean.double()[..., None]).abs() * rstd.double()[..., None], dy.double().abs()
+    size = rstd.double()[..., None] * (m + m.mean(-1, keepdim=True) + xh * (m * xh).mean(-1, keepdim=True))
+    within(a["dx"], c["dx"].double(), 2 * half(BF) * c["dx"].double().abs() + 256 * U * size, "dx")
+    within(a["dweight"], c["dweight"].double(), 256 * U * (m * xh).sum((0, 1)), "dweight")
+    within(a["dbias"], c["dbias"].double(), 256 * U * m.sum((0, 1)), "dbias")
     only = mpq.layer_norm_backward(dy, x, mean, rstd, dweight=False, dbias=False)
-    assert set(only) == {"dx"} and torch.equal(only["dx"], a["dx"])
+    assert set(only) == {"dx"}
+    within(only["dx"], c["dx"].double(), 2 * half(BF) * c["dx"].double().abs() + 256 * U * size, "dx alone")
     # a constant row has variance 0: y is the bias; a NaN stays in its row
     z = torch.full((3, n), 2.5, device="cuda", dtype=F32)
     z[1, n // 2] = math.nan
