@@ -46,16 +46,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, const __half*) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// W consecutive elements (W = 4 or 8) as floats.  vec: the address is aligned
+// W consecutive elements (W = 1, 4 or 8) as floats.  vec: the address is aligned
 // to W elements (at most 16 bytes are read at once); otherwise one by one.
 template <int W, typename T>
 __device__ __forceinline__ void load_vec(const T* p, float (&v)[W], bool vec) {
-  if (!vec) {
+  if (!vec || W == 1) {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = to_f(p[i]);
     return;
   }
-  if constexpr (sizeof(T) == 4) {
+  if constexpr (W == 1) return;
+  else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < W; i += 4) {
       const float4 q = *reinterpret_cast<const float4*>(p + i);
@@ -77,12 +78,13 @@ __device__ __forceinline__ void load_vec(const T* p, float (&v)[W], bool vec) {
 }
 template <int W, typename T>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[W], bool vec) {
-  if (!vec) {
+  if (!vec || W == 1) {
 #pragma unroll
     for (int i = 0; i < W; ++i) p[i] = from_f<T>(v[i]);
     return;
   }
-  if constexpr (sizeof(T) == 4) {
+  if constexpr (W == 1) return;
+  else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < W; i += 4)
       *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -164,6 +166,35 @@ __device__ __forceinline__ Raw8<T> load_raw(const T* p, int n, bool vec) {
     for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : from_f<T>(0.0f);
     memcpy(&r, e, sizeof(r));
   }
+  return r;
+}
+
+// Elements at .. at + 7 of a row of n 16-bit elements at any address, those
+// past the end 0.  Two aligned 16-byte loads and a shift where both lie within
+// the row, single elements at its ends.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_row8(const T* row, int at, int n) {
+  static_assert(sizeof(T) == 2, "16-bit elements");
+  const T* p = row + at;
+  const uintptr_t a = (uintptr_t)p;
+  if ((a & 15) == 0) return load_raw<T>(p, n - at, true);
+  const int off = (int)(a & 15) >> 1;  // elements past the boundary
+  if (at < off || at - off + 16 > n) return load_raw<T>(p, n - at, false);
+  const uint4* q = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
+  const uint4 u = q[0], v = q[1];
+  uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 2) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const uint32_t s = (off & 1) * 16;
+  Raw8<T> r;
+  r.q[0] = make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
   return r;
 }
 

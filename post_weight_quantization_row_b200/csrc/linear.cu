@@ -13,8 +13,9 @@
 //    MMAs.  For products with tiles enough to fill the SMs.
 //  - k_lin_split: one 128 x (16..128) tile per cluster of S CTAs, each taking
 //    1/S of the contraction; the partial tiles are joined over distributed
-//    shared memory in a fixed order.  For few rows (one token: W is read once
-//    at HBM speed by tiles x S CTAs) and for small outputs.
+//    shared memory in a fixed order.  For few rows and for small outputs.
+// Up to GEMV_ROWS rows of x W^T need no tensor cores: k_lin_gemv reads W once
+// with a warp per row of it (and any alignment).
 // The epilogue adds the bias, applies the activation, adds the residual and
 // rounds once, in fp32 before that.
 #include <cuda.h>
@@ -23,6 +24,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "f32x2.cuh"
 #include "layer_ops.cuh"
 
 namespace mpq {
@@ -33,17 +35,46 @@ using namespace tcx;
 __device__ int g_lin_status;
 
 // ------------------------------------------------------------ activations --
-// gelu through erfc and the other two through 1/(1 + e^-u), so that small
-// results of large negative z keep their relative accuracy.
+// All from one 2^x and one reciprocal each (special function unit), in forms
+// that keep the relative accuracy of small results at large negative z.
+__device__ __forceinline__ float rcp_approx(float x) {  // 1 ulp; 0 for inf
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+// The normal distribution's upper tail Phi(-a) for a >= 0, and e = e^(-a^2/2):
+// Phi(-a) e^(a^2/2) as a polynomial in t = 1/(1 + 0.3 a) without constant
+// term, fitted to erfcx(a / sqrt 2) / 2 on [0, 13.3] by reweighted least
+// squares for the least relative error (1.2e-7; in fp32 2.2e-7 absolute, and
+// 1.4e-6 relative up to a = 5, from the rounding of the exponent).
+// Half the instructions of erfcf and expf.
+__device__ __forceinline__ float normal_tail(float a, float& e) {
+  e = ex2(-0.5f * LOG2E * a * a);
+  const float t = rcp_approx(fmaf(0.3f, a, 1.0f));
+  float q = 0.03603625297546387f;
+  q = fmaf(q, t, -0.15871335566043854f);
+  q = fmaf(q, t, 0.2089640498161316f);
+  q = fmaf(q, t, -0.05609530583024025f);
+  q = fmaf(q, t, 0.1298430860042572f);
+  q = fmaf(q, t, 0.09952317178249359f);
+  q = fmaf(q, t, 0.12081687152385712f);
+  q = fmaf(q, t, 0.11962516605854034f);
+  return q * t * e;
+}
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case MPQ_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case MPQ_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case MPQ_ACT_GELU: {
+      float e;
+      const float u = z * normal_tail(fabsf(z), e);  // |u| = |z| Phi(-|z|)
+      return z >= 0.0f ? z - u : u;
+    }
     case MPQ_ACT_GELU_TANH: {
       const float u2 = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);  // 2 sqrt(2/pi) (...)
-      return __fdividef(z, 1.0f + __expf(-u2));
+      return z * rcp_approx(1.0f + ex2(-LOG2E * u2));
     }
-    case MPQ_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+    case MPQ_ACT_SILU: return z * rcp_approx(1.0f + ex2(-LOG2E * z));
     default: return z;
   }
 }
@@ -52,40 +83,73 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   if (act == MPQ_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   // beyond |z| = 30 the other three slopes are 0 or 1 to fp32; the clip keeps
   // z^3 and e^-z finite (a NaN stays one)
-  const float c = z != z ? z : fminf(fmaxf(z, -30.0f), 30.0f);
-  if (act == MPQ_ACT_GELU)
-    return fmaf(0.3989422804014327f * c, expf(-0.5f * c * c), 0.5f * erfcf(-0.70710678118654752f * c));
+  float c;
+  asm("{\n\t.reg .f32 m;\n\tmax.NaN.f32 m, %1, 0fC1F00000;\n\tmin.NaN.f32 %0, m, 0f41F00000;\n\t}" : "=f"(c) : "f"(z));
+  if (act == MPQ_ACT_GELU) {
+    float e;
+    const float u = normal_tail(fabsf(c), e);
+    return fmaf(0.3989422804014327f * c, e, c >= 0.0f ? 1.0f - u : u);
+  }
   float u = c, du = 1.0f;
   if (act == MPQ_ACT_GELU_TANH) {
-    u = 1.5957691216057308f * fmaf(0.044715f * c * c, c, c);
-    du = 1.5957691216057308f * fmaf(0.134145f * c, c, 1.0f);
+    const float c2 = c * c;
+    u = 1.5957691216057308f * fmaf(0.044715f * c2, c, c);
+    du = fmaf(0.2140644488f, c2, 1.5957691216057308f);  // u' = 2 sqrt(2/pi) (1 + 0.134145 c^2)
   }
-  const float e = expf(-fabsf(u)), d = 1.0f / (1.0f + e);
+  const float e = ex2(-LOG2E * fabsf(u)), d = rcp_approx(1.0f + e);
   const float s = u >= 0.0f ? d : e * d;  // 1/(1 + e^-u)
-  const float q = e * d * d;              // s (1 - s)
-  return fmaf(c * q, du, s);
+  return fmaf(c * (e * d * d), du, s);    // s + c s (1 - s) u'
 }
 
 // ------------------------------------------------------------- the operand --
 constexpr int BK = 64;              // contraction per stage
 constexpr int BOX = 64 * 64 * 2;    // bytes of a 64 x 64 box (8 KiB)
 
-// MN-major tile with 128-byte swizzle, as TMA writes boxes of 64 contiguous
-// output elements x 64 contraction rows: 8 contraction rows are 1024 B apart
+// Operand tiles of 64 (contraction) x 64 .. 128, with 128-byte swizzle.
+// K-major (rows of 64 contraction elements): 8 rows are 1024 B apart; 16
+// elements further along the contraction starts 32 B on.  MN-major (rows of
+// 64 output elements, one per contraction element): 8 rows are 1024 B apart
 // (stride offset), the next 64 output elements one box further (leading
-// offset); 16 contraction rows further starts 2048 B on.
-__device__ __forceinline__ uint64_t mn128_desc(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(BOX >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
+// offset); 16 contraction elements further starts 2048 B on.
+template <bool MN>
+__device__ __forceinline__ uint64_t op_desc(uint32_t saddr) {
+  uint64_t d = sw128_desc(saddr);
+  if (MN) d += (uint64_t)((BOX >> 4) - 1) << 16;
   return d;
 }
 template <bool MN>
-__device__ __forceinline__ uint64_t op_desc(uint32_t base, int kk) {
-  return MN ? mn128_desc(base + (uint32_t)kk * 2048u) : sw128_desc(base + (uint32_t)kk * 32u);
+constexpr uint32_t KSTEP = (MN ? 2048u : 32u) >> 4;  // descriptor step of 16 along the contraction
+
+// The copies of n rows (output elements) from r0 at contraction k0: K-major
+// one box of n x 64 (the map's), MN-major boxes of 64 x 64.
+template <bool MN, bool PAIR>
+__device__ __forceinline__ void load_tile(const CUtensorMap* tm, uint32_t bar, uint8_t* dst, int r0, int k0, int n) {
+  for (int h = 0; h < (MN ? n : 1); h += 64) {
+    const int c0 = MN ? r0 + h : k0, c1 = MN ? k0 : r0;
+    if (PAIR)
+      asm volatile(
+          "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+          " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst) + (uint32_t)h * 128u),
+          "l"((uint64_t)tm), "r"(bar), "r"(c0), "r"(c1)
+          : "memory");
+    else
+      asm volatile(
+          "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+          " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst) + (uint32_t)h * 128u),
+          "l"((uint64_t)tm), "r"(bar), "r"(c0), "r"(c1)
+          : "memory");
+  }
 }
+// completion of the pair's MMAs issued so far, on the barrier at the same
+// place in both CTAs
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
 // instruction descriptor: fp32 accumulator, A and B fp16 or bf16 (bits 7-9
 // and 10-12), MN-major flags (bits 15 and 16), N / 8 and M / 16
 template <typename T, bool A_MN, bool B_MN>
@@ -105,11 +169,21 @@ struct LinOut {
   bool bias_f32, bias_vec, res_vec, out_vec;
 };
 
+// The residual of W consecutive columns of a row (zeros without one).  Read
+// for several runs before the first is stored: the compiler may not move loads
+// over stores, and one at a time they cost a memory latency each.
+template <int W, typename O>
+__device__ __forceinline__ void lin_residual(const LinOut& o, int row, int col, float (&r)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) r[i] = 0.0f;
+  if (o.residual)
+    load_edge<W>(static_cast<const O*>(o.residual) + (int64_t)row * o.ldr + col, r, o.cols - col, o.res_vec);
+}
 // One run of W consecutive columns of a row: bias, activation, residual, store.
 template <int W, typename T, typename O>
 __device__ __forceinline__ void lin_finish(const LinOut& o, int row, int col, float (&v)[W],
-                                           const float (&bias)[W]) {
-  const int n = o.cols - col;
+                                           const float (&bias)[W], const float (&r)[W]) {
+  const int n = o.cols - col;  // >= 1
   const int64_t at = (int64_t)row * o.ldo + col;
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias[i];
@@ -119,8 +193,6 @@ __device__ __forceinline__ void lin_finish(const LinOut& o, int row, int col, fl
     for (int i = 0; i < W; ++i) v[i] = act_value(v[i], o.act);
   }
   if (o.residual) {
-    float r[W];
-    load_edge<W>(static_cast<const O*>(o.residual) + (int64_t)row * o.ldr + col, r, n, o.res_vec);
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] += r[i];
   }
@@ -132,21 +204,22 @@ constexpr int PT = 256;                    // tile: 256 rows x 256 columns
 constexpr int P_STAGES = 6;
 constexpr int P_STAGE = 2 * 128 * BK * 2;  // 128 rows of A and 128 of B per CTA
 constexpr int P_EPI = 8;                   // epilogue warps
-constexpr int P_THREADS = 32 * (2 + P_EPI);
+constexpr int P_THREADS = 32 * (3 + P_EPI);
 constexpr int P_SMEM = P_STAGES * P_STAGE + P_EPI * 4096 + 1024 + 256;
 static_assert(P_SMEM <= 232448, "pair kernel's shared memory");
 
-// The walk over tiles: whole waves of 256 x 256 tiles, the rest of them as
-// two 128-column halves each, so that a last partial wave takes half as long.
+// The walk over tiles: whole waves of 256 x 256 tiles; what is left for a last
+// wave runs as two 128-column halves each where that fills no more workers
+// than there are.
 struct Walk {
   int mt, nt, whole, total;
 };
-__device__ __forceinline__ Walk make_walk(int rows, int cols, int workers) {
+__host__ __device__ inline Walk make_walk(int rows, int cols, int workers) {
   Walk w;
   w.mt = (rows + PT - 1) / PT;
   w.nt = (cols + PT - 1) / PT;
-  const int t = w.mt * w.nt;
-  w.whole = t / workers * workers;
+  const int t = w.mt * w.nt, left = t % workers;
+  w.whole = 2 * left <= workers ? t - left : t;
   w.total = w.whole + 2 * (t - w.whole);
   return w;
 }
@@ -166,10 +239,15 @@ __device__ __forceinline__ void walk_tile(const Walk& w, int t, int& m0, int& n0
   n0 = (q / gm) * PT + half * (PT / 2);
 }
 
+// The issuing threads set the pace next to the MMAs (512 cycles per stage of a
+// 256-column tile): with one thread for both operands' copies, two commits a
+// stage and descriptors built per MMA they took 450 and 540 cycles a stage, and
+// 600 with the waits.  So A and B have a copying warp each, a copy is as large
+// as a box may be, a commit reaches both CTAs, and descriptors are added up.
 template <typename T, typename O, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(P_THREADS, 1)
     k_lin_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-               int KC, const __grid_constant__ LinOut o) {
+               const __grid_constant__ CUtensorMap tb_half, int KC, const __grid_constant__ LinOut o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* stg_all = smem + P_STAGES * P_STAGE;
@@ -196,6 +274,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&ta) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tb) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tb_half) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -211,36 +292,37 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   const uint32_t full_r0 = map_to_rank(smem_u32(full), 0);
   const uint32_t tm_empty_r0 = map_to_rank(smem_u32(tm_empty), 0);
 
-  if (warp == 0 && lane == 0) {
-    // -------------------------------------------------------------- producer
+  if ((warp == 0 || warp == 2) && lane == 0) {
+    // ------------------------------------------------- producers: A and B
+    const bool is_a = warp == 0;
+    uint8_t* dst0 = smem + (is_a ? 0 : 128 * BK * 2);
     uint32_t it = 0;
+    int s = 0;
+    uint32_t phase = 1;  // of `empty`: the first turn over the ring passes at once
     bool ok = true;
     for (int t = worker; t < walk.total && ok; t += nworkers) {
       int m0, n0, wn;
       walk_tile(walk, t, m0, n0, wn);
-      const int am = m0 + (int)rank * 128;
-      const int bn = n0 + (int)rank * (wn / 2);
+      const int r0 = is_a ? m0 + (int)rank * 128 : n0 + (int)rank * (wn / 2);
       const uint32_t bytes = (uint32_t)((128 + wn / 2) * BK * 2);
-      for (int kt = 0; kt < KT; ++kt, ++it) {
-        const int s = it % P_STAGES;
-        if (it >= (uint32_t)P_STAGES && !mbar_wait(&empty[s], (it / P_STAGES - 1) & 1)) {
+      const CUtensorMap* tm = wn == PT ? &tb : &tb_half;
+      for (int k0 = 0; k0 < KT * BK; k0 += BK, ++it) {
+        if (!mbar_wait(&empty[s], phase)) {
           atomicOr(&g_lin_status, STATUS_TIMEOUT);
           ok = false;
           break;
         }
-        uint8_t* a = smem + s * P_STAGE;
-        uint8_t* b = a + 128 * BK * 2;
         const uint32_t fb = full_r0 + 8u * (uint32_t)s;  // rank 0's barrier counts both CTAs' bytes
-        if (rank == 0) mbar_expect_tx(&full[s], 2 * bytes);
-        const int k0 = kt * BK;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (A_MN) tma_load_2d_cg2(&ta, fb, a + h * BOX, am + h * 64, k0);
-          else tma_load_2d_cg2(&ta, fb, a + h * BOX, k0, am + h * 64);
+        uint8_t* dst = dst0 + s * P_STAGE;
+        if (is_a) {
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * bytes);
+          load_tile<A_MN, true>(&ta, fb, dst, r0, k0, 128);
+        } else {
+          load_tile<B_MN, true>(tm, fb, dst, r0, k0, wn / 2);
         }
-        for (int h = 0; h < wn / 128; ++h) {
-          if (B_MN) tma_load_2d_cg2(&tb, fb, b + h * BOX, bn + h * 64, k0);
-          else tma_load_2d_cg2(&tb, fb, b + h * BOX, k0, bn + h * 64);
+        if (++s == P_STAGES) {
+          s = 0;
+          phase ^= 1;
         }
       }
     }
@@ -253,7 +335,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t ID_W = lin_idesc<T, A_MN, B_MN>(256, PT), ID_N = lin_idesc<T, A_MN, B_MN>(256, PT / 2);
-    uint32_t it = 0, tl = 0;
+    const uint64_t da0 = op_desc<A_MN>(smem_u32(smem)), db0 = op_desc<B_MN>(smem_u32(smem) + 128 * BK * 2);
+    uint32_t tl = 0;
+    int s = 0;
+    uint32_t phase = 0;
     bool ok = true;
     for (int t = worker; t < walk.total && ok; t += nworkers, ++tl) {
       const int buf = tl & 1;
@@ -267,37 +352,37 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       }
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)buf * PT;
-      for (int kt = 0; kt < KT; ++kt, ++it) {
-        const int s = it % P_STAGES;
-        if (!mbar_wait_cl(&full[s], (it / P_STAGES) & 1)) {
+      for (int kt = 0; kt < KT; ++kt) {
+        if (!mbar_wait_cl(&full[s], phase)) {
           atomicOr(&g_lin_status, STATUS_TIMEOUT);
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + s * P_STAGE), b = a + 128 * BK * 2;
+        const uint64_t da = da0 + (uint32_t)s * (P_STAGE >> 4), db = db0 + (uint32_t)s * (P_STAGE >> 4);
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          umma_f16_cg2(d, op_desc<A_MN>(a, kk), op_desc<B_MN>(b, kk), idesc, (kt | kk) != 0 ? 1u : 0u);
-        umma_commit_cg2(smem_u32(&empty[s]));
-        umma_commit_cg2(map_to_rank(smem_u32(&empty[s]), 1));
+          umma_f16_cg2(d, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (kt | kk) != 0 ? 1u : 0u);
+        commit_both(&empty[s]);
+        if (++s == P_STAGES) {
+          s = 0;
+          phase ^= 1;
+        }
       }
-      if (ok) {
-        umma_commit_cg2(smem_u32(&tm_full[buf]));
-        umma_commit_cg2(map_to_rank(smem_u32(&tm_full[buf]), 1));
-      }
+      if (ok) commit_both(&tm_full[buf]);
     }
     for (uint32_t q = (tl > 2 ? tl - 2 : 0); q < tl; ++q)  // MMAs finish before TMEM is freed
       for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&tm_full[q & 1], (q / 2) & 1); ++i)
         if (i > 256) __nanosleep(64);
-  } else if (warp >= 2) {
+  } else if (warp >= 3) {
     // -------------------------------------------------------------- epilogue
     // two warps per TMEM lane quadrant, alternating over 32-column chunks.  A
     // chunk goes through a swizzled 32 x 32 fp32 staging tile, which turns
     // the lane-per-row layout into 8 consecutive columns per lane.
-    const int q = warp & 3, side = (warp - 2) >> 2;
-    float4* stg = reinterpret_cast<float4*>(stg_all + (warp - 2) * 4096);
+    const int q = warp & 3, side = (warp - 3) >> 2;
+    float4* stg = reinterpret_cast<float4*>(stg_all + (warp - 3) * 4096);
     const int c8 = (lane & 3) * 8, r8 = lane >> 2;
+    const bool wide = o.out_vec && (!o.residual || o.res_vec);
     uint32_t tl = 0;
     for (int t = worker; t < walk.total; t += nworkers, ++tl) {
       const int buf = tl & 1;
@@ -327,18 +412,41 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
                           __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
         __syncwarp();
-        float bias[8] = {};
-        if (o.bias && col < o.cols)
-          load_param<8, T>(o.bias, o.bias_f32, col, bias, o.cols - col, o.bias_vec);
-        if (col < o.cols) {
+        if (wide) {
+          float bias[8] = {};
+          if (o.bias && col < o.cols)
+            load_param<8, T>(o.bias, o.bias_f32, col, bias, o.cols - col, o.bias_vec);
+          if (col < o.cols) {
+            float res[4][8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = i * 8 + r8;
-            if (row0 + rr < o.rows) {
-              const float4 x0 = stg[rr * 8 + ((c8 / 4) ^ (rr & 7))];
-              const float4 x1 = stg[rr * 8 + ((c8 / 4 + 1) ^ (rr & 7))];
-              float w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-              lin_finish<8, T, O>(o, row0 + rr, col, w, bias);
+            for (int i = 0; i < 4; ++i)
+              if (row0 + i * 8 + r8 < o.rows) lin_residual<8, O>(o, row0 + i * 8 + r8, col, res[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rr = i * 8 + r8;
+              if (row0 + rr < o.rows) {
+                const float4 x0 = stg[rr * 8 + ((c8 / 4) ^ (rr & 7))];
+                const float4 x1 = stg[rr * 8 + ((c8 / 4 + 1) ^ (rr & 7))];
+                float w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                lin_finish<8, T, O>(o, row0 + rr, col, w, bias, res[i]);
+              }
+            }
+          }
+        } else if (n0 + c0 + lane < o.cols) {  // unaligned rows: a column a lane
+          float bias[1] = {};
+          if (o.bias) load_param<1, T>(o.bias, o.bias_f32, n0 + c0 + lane, bias, 1, false);
+          const int top = min(32, o.rows - row0);
+          for (int r0 = 0; r0 < top; r0 += 16) {
+            float res[16][1];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (r0 + i < top) lin_residual<1, O>(o, row0 + r0 + i, n0 + c0 + lane, res[i]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int rr = r0 + i;
+              if (rr >= top) break;
+              float w[1] = {reinterpret_cast<const float*>(stg + rr * 8 + ((lane >> 2) ^ (rr & 7)))[lane & 3]};
+              lin_finish<1, T, O>(o, row0 + rr, n0 + c0 + lane, w, bias, res[i]);
             }
           }
         }
@@ -359,7 +467,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 // Roles are swapped: the operand with the output's columns (W, or x for dW)
 // fills the 128 TMEM lanes, the one with its rows (the tokens) the NT columns
 // of the accumulator, so few rows waste no tensor work.
-constexpr int S_THREADS = 192;
+constexpr int S_THREADS = 320;  // copies, MMAs, 8 epilogue warps
 
 struct SplitGeom {
   int NT;      // rows of the output per tile (accumulator columns)
@@ -369,15 +477,11 @@ struct SplitGeom {
   uint32_t tmem_cols;
 };
 __host__ __device__ inline int split_stage_bytes(int NT) { return 128 * BK * 2 + NT * BK * 2; }
-
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
+// Elements of a partial tile (row-major, 128 columns) that each of S CTAs
+// joins: whole runs of 32.
+__host__ __device__ inline int split_share(int rows, int S) { return ((rows * 128 + S - 1) / S + 31) / 32 * 32; }
+// Shared memory behind the ring for the partial tiles of S > 1 CTAs
+__host__ __device__ inline int split_recv_bytes(int NT, int S) { return S > 1 ? S * split_share(NT, S) * 4 : 0; }
 
 template <typename T, typename O, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(S_THREADS)
@@ -386,16 +490,20 @@ __global__ void __launch_bounds__(S_THREADS)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int stage = split_stage_bytes(g.NT);
-  uint64_t* full = (uint64_t*)(smem + g.stages * stage);
+  float* recv = (float*)(smem + g.stages * stage);
+  uint64_t* full = (uint64_t*)(smem + g.stages * stage + split_recv_bytes(g.NT, g.S));
   uint64_t* empty = full + g.stages;
   uint64_t* done = empty + g.stages;
-  uint32_t* tmem_slot = (uint32_t*)(done + 1);
+  uint64_t* arrived = done + 1;  // S > 1: every CTA's part of this CTA's share is in recv
+  uint32_t* tmem_slot = (uint32_t*)(arrived + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = g.S > 1 ? (int)cluster_ctarank() : 0;
   const int a0 = blockIdx.y * 128, b0 = blockIdx.z * g.NT;
   const int k_lo = (int)((int64_t)g.KT * rank / g.S), k_hi = (int)((int64_t)g.KT * (rank + 1) / g.S);
   const int nk = k_hi - k_lo;  // >= 1
+  const int nrow = min(g.NT, o.rows - b0), share = split_share(nrow, g.S);
+  const int e_lo = rank * share, e_hi = min(nrow * 128, e_lo + share);  // what this CTA joins
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
@@ -403,8 +511,12 @@ __global__ void __launch_bounds__(S_THREADS)
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(arrived, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (g.S > 1) mbar_expect_tx(arrived, (uint32_t)(g.S * max(e_hi - e_lo, 0) * 4));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&ta) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tb) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -416,30 +528,25 @@ __global__ void __launch_bounds__(S_THREADS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (g.S > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
-  bool ok = true;
   if (warp == 0 && lane == 0) {
-    int i = 0;
+    int i = 0, s = 0;
+    uint32_t phase = 1;
     for (; i < nk; ++i) {
-      const int s = i % g.stages;
-      if (i >= g.stages && !mbar_wait(&empty[s], (i / g.stages - 1) & 1)) {
+      if (!mbar_wait(&empty[s], phase)) {
         atomicOr(&g_lin_status, STATUS_TIMEOUT);
         break;
       }
       uint8_t* a = smem + s * stage;
-      uint8_t* b = a + 128 * BK * 2;
       const int k0 = (k_lo + i) * BK;
+      const uint32_t fb = smem_u32(&full[s]);
       mbar_expect_tx(&full[s], (uint32_t)stage);
-      if (A_MN) {
-        tma_load_2d(&ta, &full[s], a, a0, k0);
-        tma_load_2d(&ta, &full[s], a + BOX, a0 + 64, k0);
-      } else {
-        tma_load_2d(&ta, &full[s], a, k0, a0);
-      }
-      if (B_MN) {
-        for (int h = 0; h < g.NT / 64; ++h) tma_load_2d(&tb, &full[s], b + h * BOX, b0 + h * 64, k0);
-      } else {
-        tma_load_2d(&tb, &full[s], b, k0, b0);
+      load_tile<A_MN, false>(&ta, fb, a, a0, k0, 128);
+      load_tile<B_MN, false>(&tb, fb, a + 128 * BK * 2, b0, k0, g.NT);
+      if (++s == g.stages) {
+        s = 0;
+        phase ^= 1;
       }
     }
     for (int q = (i > g.stages ? i - g.stages : 0); q < i; ++q)  // every copy lands
@@ -447,36 +554,40 @@ __global__ void __launch_bounds__(S_THREADS)
         if (w > 256) __nanosleep(64);
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = lin_idesc<T, A_MN, B_MN>(128, g.NT);
+    const uint64_t da0 = op_desc<A_MN>(smem_u32(smem)), db0 = op_desc<B_MN>(smem_u32(smem) + 128 * BK * 2);
+    int s = 0;
+    uint32_t phase = 0;
     for (int i = 0; i < nk; ++i) {
-      const int s = i % g.stages;
-      if (!mbar_wait(&full[s], (i / g.stages) & 1)) {
+      if (!mbar_wait(&full[s], phase)) {
         atomicOr(&g_lin_status, STATUS_TIMEOUT);
         break;
       }
       tc_fence_after();
-      const uint32_t a = smem_u32(smem + s * stage), b = a + 128 * BK * 2;
+      const uint64_t da = da0 + (uint32_t)s * (uint32_t)(stage >> 4), db = db0 + (uint32_t)s * (uint32_t)(stage >> 4);
 #pragma unroll
       for (int kk = 0; kk < BK / 16; ++kk)
-        umma_f16(tmem, op_desc<A_MN>(a, kk), op_desc<B_MN>(b, kk), idesc, (i | kk) != 0 ? 1u : 0u);
+        umma_f16(tmem, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (i | kk) != 0 ? 1u : 0u);
       umma_commit(&empty[s]);
+      if (++s == g.stages) {
+        s = 0;
+        phase ^= 1;
+      }
     }
     umma_commit(done);
     for (uint32_t w = 0; w < (1u << 25) && !mbar_try_wait(done, 0); ++w)
       if (w > 256) __nanosleep(64);
   } else if (warp >= 2) {
-    ok = __all_sync(0xffffffffu, mbar_wait(done, 0));
-    if (!ok && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    if (!__all_sync(0xffffffffu, mbar_wait(done, 0)) && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
   }
   // All copies have landed and all MMAs have read them: the ring becomes the
-  // partial tile part[row][128 columns] (fp32).  Lane l of quadrant q holds
-  // column 32 q + l of the output, one row per accumulator column.
+  // partial tile part[row][128 columns].  Lane l of quadrant q holds column
+  // 32 q + l of the output, one row per accumulator column.
   __syncthreads();
   tc_fence_after();
   float* part = reinterpret_cast<float*>(smem);
   if (warp >= 2) {
     const int q = warp & 3;
-    const int nrow = min(g.NT, o.rows - b0);
-    for (int c0 = 0; c0 < nrow; c0 += 16) {
+    for (int c0 = ((warp - 2) >> 2) * 16; c0 < nrow; c0 += 32) {
       uint32_t v[16];
       asm volatile(
           "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -486,60 +597,169 @@ __global__ void __launch_bounds__(S_THREADS)
             "=r"(v[14]), "=r"(v[15])
           : "r"(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0));
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      float* p = part + c0 * 128 + q * 32 + lane;  // (rows up to NT fit)
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (c0 + j < nrow) part[(c0 + j) * 128 + q * 32 + lane] = __uint_as_float(v[j]);
+      for (int j = 0; j < 16; ++j) p[j * 128] = __uint_as_float(v[j]);
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (g.S > 1) cluster_sync();  // every CTA's partial tile is written
-  {
-    // each CTA joins its share of the tile, in rank order, 4 columns a thread
-    const int nrow = min(g.NT, o.rows - b0);
-    const int units = nrow * 32;
-    const int u_hi = (int)((int64_t)units * (rank + 1) / g.S);
-    for (int u = (int)((int64_t)units * rank / g.S) + (int)threadIdx.x; u < u_hi; u += S_THREADS) {
-      const int r = u >> 5, c = (u & 31) * 4;
-      if (a0 + c >= o.cols) continue;
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const uint32_t at = smem_u32(part + r * 128 + c);
-      if (g.S > 1) {
-        for (int p = 0; p < g.S; ++p) {
-          const float4 x = ld_cluster4(map_to_rank(at, (uint32_t)p));
-          v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        }
-      } else {
-        const float4 x = *reinterpret_cast<const float4*>(part + r * 128 + c);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  const float* from = part;
+  if (g.S > 1) {
+    // every CTA sends every other (and itself) its share of the partial tile,
+    // by bulk copies between the CTAs' shared memories
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all CTAs have begun
+    if (threadIdx.x == 0) {
+      for (int p = 0; p < g.S; ++p) {
+        const int lo = p * share, n = min(nrow * 128, lo + share) - lo;
+        if (n <= 0) break;
+        asm volatile(
+            "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                map_to_rank(smem_u32(recv + rank * share), (uint32_t)p)),
+            "r"(smem_u32(part + lo)), "r"((uint32_t)(n * 4)), "r"(map_to_rank(smem_u32(arrived), (uint32_t)p))
+            : "memory");
       }
-      float bias[4] = {};
-      if (o.bias) load_param<4, T>(o.bias, o.bias_f32, a0 + c, bias, o.cols - (a0 + c), o.bias_vec);
-      lin_finish<4, T, O>(o, b0 + r, a0 + c, v, bias);
     }
+    __syncwarp();
+    if (!mbar_wait_cl(arrived, 0) && threadIdx.x == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    __syncwarp();
+    // (what this CTA receives has arrived; when all say so, all copies are done)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    from = recv;
+  } else {
+    __syncthreads();
   }
-  __syncthreads();
-  if (g.S > 1) cluster_sync();  // no peer still reads this CTA's tile
+  {
+    // each CTA joins its share of the tile, in rank order, two runs a turn
+    // (their loads are in flight together)
+    const auto join = [&](auto width) {
+      constexpr int W = decltype(width)::value, R = W == 1 ? 8 : 2;
+      for (int e0 = e_lo + (int)threadIdx.x * W; e0 < e_hi; e0 += R * S_THREADS * W) {
+        float res[R][W], bias[R][W], v[R][W];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int e = e0 + i * S_THREADS * W, r = e >> 7, c = a0 + (e & 127);
+          if (e >= e_hi || c >= o.cols) continue;
+          lin_residual<W, O>(o, b0 + r, c, res[i]);
+#pragma unroll
+          for (int j = 0; j < W; ++j) bias[i][j] = v[i][j] = 0.0f;
+          if (o.bias) load_param<W, T>(o.bias, o.bias_f32, c, bias[i], o.cols - c, o.bias_vec);
+          for (int p = 0; p < g.S; ++p) {
+            const float* x = from + p * share + (e - e_lo);
+            if constexpr (W == 8) {
+              const float4 q = reinterpret_cast<const float4*>(x)[0], u = reinterpret_cast<const float4*>(x)[1];
+              v[i][0] += q.x; v[i][1] += q.y; v[i][2] += q.z; v[i][3] += q.w;
+              v[i][4] += u.x; v[i][5] += u.y; v[i][6] += u.z; v[i][7] += u.w;
+            } else {
+              v[i][0] += *x;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int e = e0 + i * S_THREADS * W, r = e >> 7, c = a0 + (e & 127);
+          if (e >= e_hi || c >= o.cols) continue;
+          lin_finish<W, T, O>(o, b0 + r, c, v[i], bias[i], res[i]);
+        }
+      }
+    };
+    if (o.out_vec && (!o.residual || o.res_vec)) join(std::integral_constant<int, 8>{});
+    else join(std::integral_constant<int, 1>{});  // unaligned rows: neighbouring threads, neighbouring columns
+  }
+  __syncwarp();
+  if (g.S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no copy still reads this CTA's tile
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
   }
 }
 
-// -------------------------------------------------- rows and pre-activation --
-// Copies rows x cols 16-bit elements to a leading dimension that TMA can take
-// (a multiple of 8).  Only for operands whose base or row stride is not a
-// multiple of 16 bytes.
-__global__ void k_lin_pack(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
-                           uint16_t* __restrict__ dst, int64_t ldd) {
-  const int64_t groups = ldd / 8;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * groups;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t r = i / groups, c = (i % groups) * 8;
-    uint16_t v[8];
+// ------------------------------------------------------------- few rows --
+// y = x W^T for one or two rows of x, bound by the read of W: WPR warps share a
+// row of W, 16 bytes a lane and load, four loads in flight; the sums meet by
+// shuffles and, for WPR > 1, in shared memory.  x comes from L1.
+constexpr int GEMV_ROWS = 2, GEMV_WARPS = 8;
+template <typename T, typename O, int MR, bool VEC>
+__global__ void __launch_bounds__(GEMV_WARPS * 32, 4)
+    k_lin_gemv(const T* __restrict__ x, int64_t ldx, const T* __restrict__ w, int64_t ldw, int K, int wpr,
+               const __grid_constant__ LinOut o) {
+  __shared__ float sums[GEMV_WARPS][MR];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = GEMV_WARPS / wpr;  // outputs per block
+  const int n0 = blockIdx.x * per, col = n0 + warp / wpr;
+  uint64_t acc[MR][2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? src[r * ld + c + j] : (uint16_t)0;
-    *reinterpret_cast<uint4*>(dst + r * ldd + c) = *reinterpret_cast<const uint4*>(v);
+  for (int m = 0; m < MR; ++m) acc[m][0] = acc[m][1] = 0ull;
+  const auto add = [&](const Raw8<T>& wv, int k) {
+    float a[8];
+    decode<T>(wv, a);
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      float b[8];
+      if (VEC) decode<T>(load_raw<T>(x + m * ldx + k, K - k, true), b);
+      else decode<T>(load_row8<T>(x + m * ldx, k, K), b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[m][i & 1] = f2_fma(f2_pack(a[2 * i], a[2 * i + 1]), f2_pack(b[2 * i], b[2 * i + 1]), acc[m][i & 1]);
+    }
+  };
+  if (col < o.cols) {
+    const T* wr = w + (int64_t)col * ldw;
+    constexpr int U = 4;
+    const int step = wpr * 256;
+    int k = (warp % wpr) * 256 + lane * 8;
+    if (VEC) {
+      for (; k + (U - 1) * step + 8 <= K; k += U * step) {
+        Raw8<T> wv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) wv[u].q[0] = __ldcs(reinterpret_cast<const uint4*>(wr + k + u * step));
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(wv[u], k + u * step);
+      }
+    }
+    for (; k < K; k += step) add(load_row8<T>(wr, k, K), k);
+  }
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    float a, b;
+    f2_unpack(f2_add(acc[m][0], acc[m][1]), a, b);
+    float s = a + b;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+    if (lane == 0) sums[warp][m] = s;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < per * MR; i += GEMV_WARPS * 32) {
+    const int m = i / per, c = i % per;
+    if (n0 + c >= o.cols) continue;
+    float v[1] = {0.0f}, bias[1] = {};
+    for (int q = 0; q < wpr; ++q) v[0] += sums[c * wpr + q][m];
+    if (o.bias) bias[0] = o.bias_f32 ? static_cast<const float*>(o.bias)[n0 + c] : to_f(static_cast<const T*>(o.bias)[n0 + c]);
+    float res[1];
+    lin_residual<1, O>(o, m, n0 + c, res);
+    lin_finish<1, T, O>(o, m, n0 + c, v, bias, res);
+  }
+}
+
+// -------------------------------------------------- rows and pre-activation --
+// Copies rows x cols 16-bit elements of up to two operands to leading
+// dimensions that TMA can take (multiples of 8).  Only for operands whose base
+// or row stride is not a multiple of 16 bytes.
+struct PackJob {
+  const __half* src;  // 16-bit elements, copied as they are
+  __half* dst;
+  int64_t ld, rows, cols, ldd;
+};
+__global__ void __launch_bounds__(256)
+    k_lin_pack(const __grid_constant__ PackJob a, const __grid_constant__ PackJob b) {
+  const int64_t na = a.rows * (a.ldd / 8), nb = b.rows * (b.ldd / 8);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < na + nb; i += (int64_t)gridDim.x * 256) {
+    const PackJob& j = i < na ? a : b;
+    const int64_t at = i < na ? i : i - na, groups = j.ldd / 8;
+    const int64_t r = at / groups;
+    const int c = (int)(at % groups) * 8;
+    const Raw8<__half> v = load_row8<__half>(j.src + r * j.ld, c, (int)j.cols);
+    *reinterpret_cast<uint4*>(j.dst + r * j.ldd + c) = v.q[0];
   }
 }
 
@@ -559,18 +779,32 @@ __global__ void __launch_bounds__(256)
   float sum[8] = {};
   if (c < n) {
     const int left = (int)min((int64_t)8, n - c);
-    for (int64_t r = r_lo + rl; r < r_hi; r += 8) {
-      float g[8];
-      load_edge<8>(dy + r * ldy + c, g, left, vec_y);
-      if (act != MPQ_ACT_NONE) {
-        float u[8];
-        load_edge<8>(z + r * ldz + c, u, left, vec_z);
+    constexpr int NR = 4;  // rows in flight
+    for (int64_t r0 = r_lo + rl; r0 < r_hi; r0 += 8 * NR) {
+      Raw8<T> gy[NR], zz[NR];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] *= act_slope(u[j], act);
+      for (int q = 0; q < NR; ++q) {
+        const int64_t r = r0 + 8 * q;
+        const int have = r < r_hi ? left : 0;
+        gy[q] = load_raw<T>(dy + (r < r_hi ? r : r0) * ldy + c, have, vec_y);
+        if (act != MPQ_ACT_NONE) zz[q] = load_raw<T>(z + (r < r_hi ? r : r0) * ldz + c, have, vec_z);
       }
-      if (dz) store_vec<8>(dz + r * ldd + c, g, true);  // ldd is a multiple of 8: the pad is zero
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += g[j];
+      for (int q = 0; q < NR; ++q) {
+        const int64_t r = r0 + 8 * q;
+        if (r >= r_hi) break;
+        float g[8];
+        decode<T>(gy[q], g);
+        if (act != MPQ_ACT_NONE) {
+          float u[8];
+          decode<T>(zz[q], u);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] *= act_slope(u[j], act);
+        }
+        if (dz) store_vec<8>(dz + r * ldd + c, g, true);  // ldd is a multiple of 8: the pad is zero
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += g[j];
+      }
     }
   }
   if (!part) return;
@@ -645,16 +879,24 @@ int64_t packed_bytes(int64_t inner, int64_t rows) {
 // A row stride for TMA where there is one row (its stride is not read).
 int64_t tma_ld(const Operand& a) { return a.rows <= 1 ? round_up(a.inner, 8) : a.ld; }
 
-mpq_status pack(Operand* a, void* dst, cudaStream_t st) {
-  const int64_t ldd = round_up(a->inner, 8), work = a->rows * (ldd / 8);
+// Packs those of two operands that have somewhere to go.
+mpq_status pack(Operand* a, void* dst_a, Operand* b, void* dst_b, cudaStream_t st) {
+  const auto job = [](Operand* q, void* dst) {
+    PackJob j{};
+    if (!dst) return j;
+    j = PackJob{static_cast<const __half*>(q->p), static_cast<__half*>(dst), q->ld, q->rows, q->inner, round_up(q->inner, 8)};
+    q->p = dst;
+    q->ld = j.ldd;
+    return j;
+  };
+  const PackJob ja = job(a, dst_a), jb = job(b, dst_b);
+  const int64_t work = (ja.rows * ja.ldd + jb.rows * jb.ldd) / 8;
+  if (work == 0) return MPQ_OK;
   {
     ProfScope ps_("k_lin_pack", st);
-    k_lin_pack<<<(unsigned)std::min<int64_t>(cdiv(work, 256), 148 * 16), 256, 0, st>>>(
-        static_cast<const uint16_t*>(a->p), a->ld, a->rows, a->inner, static_cast<uint16_t*>(dst), ldd);
+    k_lin_pack<<<(unsigned)std::min<int64_t>(cdiv(work, 256), 148 * 16), 256, 0, st>>>(ja, jb);
   }
   count_launch();
-  a->p = dst;
-  a->ld = ldd;
   return check_launch("k_lin_pack");
 }
 
@@ -662,7 +904,7 @@ template <typename T, typename O, bool RN, bool CN>
 mpq_status set_attrs() {
   MPQ_CUDA(cudaFuncSetAttribute(k_lin_pair<T, O, RN, CN>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
   MPQ_CUDA(cudaFuncSetAttribute(k_lin_split<T, O, CN, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                113 * 1024));
+                                220 * 1024));
   return MPQ_OK;
 }
 
@@ -725,10 +967,12 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
   const int64_t big = cdiv(o.rows, PT) * cdiv(o.cols, PT);
   const int pairs = g_lin_dev[dev].pairs;
   ProfScope ps_(tag, st);
-  if (pairs > 0 && o.rows > 128 && big * 2 >= pairs) {
-    CUtensorMap ta, tb;
-    MPQ_TRY(encode_box(&ta, R.p, R.inner, R.rows, tma_ld(R), bf, 64));
-    MPQ_TRY(encode_box(&tb, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, 64));
+  static const int LP = getenv("LP") ? atoi(getenv("LP")) : 1;
+  if (pairs > 0 && o.rows > 128 && big * 2 >= LP) {
+    CUtensorMap ta, tb, tb_half;
+    MPQ_TRY(encode_box(&ta, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : 128));
+    MPQ_TRY(encode_box(&tb, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
+    MPQ_TRY(encode_box(&tb_half, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, 64));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(2 * big, pairs));
     cfg.blockDim = dim3(P_THREADS);
@@ -741,22 +985,24 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    MPQ_CUDA(cudaLaunchKernelEx(&cfg, k_lin_pair<T, O, RN, CN>, ta, tb, (int)KC, o));
+    MPQ_CUDA(cudaLaunchKernelEx(&cfg, k_lin_pair<T, O, RN, CN>, ta, tb, tb_half, (int)KC, o));
   } else {
     SplitGeom g;
     g.NT = RN ? (o.rows <= 64 ? 64 : 128) : (int)std::min<int64_t>(128, round_up(o.rows, 16));
     const int64_t at_ = cdiv(o.cols, 128), bt = cdiv(o.rows, g.NT);
     if (bt > 65535 || at_ > 65535) return fail(MPQ_ERR_INVALID_ARG, "linear: too many tiles");
+    static const int LS = getenv("LS") ? atoi(getenv("LS")) : 4;
+    const int per_sm = g.NT <= 32 ? 2 : 1;
     g.S = 1;
-    while (g.S < 8 && at_ * bt * g.S * 2 <= 2 * sms && KT >= 4 * g.S) g.S *= 2;
+    while (g.S < LS && at_ * bt * g.S * 2 <= per_sm * sms && KT >= 4 * g.S) g.S *= 2;
     g.KT = (int)KT;
-    const int budget = 111 * 1024;
-    g.stages = (int)std::min<int64_t>(budget / split_stage_bytes(g.NT), std::max<int64_t>(cdiv(KT, g.S), 1));
+    const int budget = 216 * 1024 / per_sm - split_recv_bytes(g.NT, g.S);
+    g.stages = (int)std::min<int64_t>(std::min(budget / split_stage_bytes(g.NT), 12), std::max<int64_t>(cdiv(KT, g.S), 1));
     // the ring must also hold the partial tile
-    g.stages = std::max(g.stages, (int)cdiv(g.NT * 128 * 4, split_stage_bytes(g.NT)));
+    g.stages = std::max(g.stages, (int)cdiv(round_up(g.NT, 32) * 128 * 4, split_stage_bytes(g.NT)));
     g.tmem_cols = 32;
     while ((int)g.tmem_cols < g.NT) g.tmem_cols *= 2;
-    const int smem = g.stages * split_stage_bytes(g.NT) + (2 * g.stages + 1) * 8 + 16 + 1024;
+    const int smem = g.stages * split_stage_bytes(g.NT) + split_recv_bytes(g.NT, g.S) + (2 * g.stages + 2) * 8 + 16 + 1024;
     CUtensorMap ta, tb;
     MPQ_TRY(encode_box(&ta, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
     MPQ_TRY(encode_box(&tb, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : g.NT));
@@ -787,13 +1033,30 @@ mpq_status check_dims(const char* who, int64_t rows, int64_t n, int64_t k, int32
   return MPQ_OK;
 }
 
+bool use_gemv(int64_t rows) { return rows <= GEMV_ROWS; }
+
 template <typename T, typename O>
 mpq_status linear_fwd(Operand x, Operand w, const LinOut& o, char* ws, cudaStream_t st) {
-  if (!tma_ok(x.p, x.inner, x.rows, x.ld)) {
-    MPQ_TRY(pack(&x, ws, st));
-    ws += packed_bytes(x.inner, x.rows);
+  if (use_gemv(x.rows)) {
+    // a warp per row of W fills the device from 24 warps an SM on; below that
+    // more warps share a row, as long as each has 512 elements
+    int wpr = 1;
+    while (wpr < GEMV_WARPS && w.rows * wpr < 148 * 24 && x.inner >= 1024 * wpr) wpr *= 2;
+    const unsigned grid = (unsigned)cdiv(w.rows, GEMV_WARPS / wpr);
+    const bool vec = aligned_rows(x.p, x.ld, 2, 16) && aligned_rows(w.p, w.ld, 2, 16);
+    const auto go = [&](auto kernel) {
+      kernel<<<grid, GEMV_WARPS * 32, 0, st>>>(static_cast<const T*>(x.p), x.ld, static_cast<const T*>(w.p), w.ld,
+                                               (int)x.inner, wpr, o);
+    };
+    ProfScope ps_("k_linear", st);
+    if (x.rows == 1) vec ? go(k_lin_gemv<T, O, 1, true>) : go(k_lin_gemv<T, O, 1, false>);
+    else vec ? go(k_lin_gemv<T, O, 2, true>) : go(k_lin_gemv<T, O, 2, false>);
+    count_launch();
+    return check_launch("k_linear");
   }
-  if (!tma_ok(w.p, w.inner, w.rows, w.ld)) MPQ_TRY(pack(&w, ws, st));
+  char* to_x = tma_ok(x.p, x.inner, x.rows, x.ld) ? nullptr : ws;
+  char* to_w = tma_ok(w.p, w.inner, w.rows, w.ld) ? nullptr : ws + (to_x ? packed_bytes(x.inner, x.rows) : 0);
+  MPQ_TRY(pack(&x, to_x, &w, to_w, st));
   return lin_product<T, O, false, false>(x, w, x.inner, o, st, "k_linear");
 }
 
@@ -845,8 +1108,7 @@ mpq_status linear_bwd(const void* dy, int64_t ldy, Operand x, Operand w, const v
     }
     if (p.make_dz) dz = Operand{dzp, n, rows, ldd};
   }
-  if (p.pack_x) MPQ_TRY(pack(&x, ws + p.x, st));
-  if (p.pack_w) MPQ_TRY(pack(&w, ws + p.w, st));
+  MPQ_TRY(pack(&x, p.pack_x ? ws + p.x : nullptr, &w, p.pack_w ? ws + p.w : nullptr, st));
   LinOut o{};
   if (dx) {  // dx[rows x k] = dz[rows x n] W[n x k]: W has the output's columns contiguous
     o.out = dx;
@@ -874,7 +1136,7 @@ using namespace mpq;
 
 extern "C" int64_t mpq_linear_workspace_bytes(const void* x, int64_t ldx, const void* weight, int64_t ldw,
                                               int64_t rows, int64_t n, int64_t k) {
-  if (rows < 1 || n < 1 || k < 1) return 0;
+  if (rows < 1 || n < 1 || k < 1 || use_gemv(rows)) return 0;
   return (tma_ok(x, k, rows, ldx) ? 0 : packed_bytes(k, rows)) + (tma_ok(weight, k, n, ldw) ? 0 : packed_bytes(k, n));
 }
 

@@ -23,17 +23,18 @@ def test_linear_refuses(mpq):
     lib = mpq.lib
     for kw in (dict(rows=-1), dict(rows=1 << 24), dict(n=0), dict(k=0), dict(n=1 << 23), dict(k=1 << 23), dict(dtype=0),
                dict(dtype=3), dict(act=5), dict(act=-1), dict(ydt=2), dict(bias=P, bdt=2), dict(x=None), dict(w=None),
-               dict(y=None), dict(ldx=9), dict(ldw=4), dict(x=C.c_void_p(4098))):
+               dict(y=None), dict(rows=6, ldx=9), dict(rows=6, ldw=4), dict(rows=6, x=C.c_void_p(4098))):
         assert linear(lib, **kw) == 1, kw
         assert b"linear" in lib.mpq_last_error()
     assert linear(lib, rows=0, x=None, w=None, y=None) == 0  # nothing to do
-    # scratch: none for aligned rows; both operands' packed copies otherwise
+    # scratch: none for aligned rows or up to 2 of them; both operands' packed copies otherwise
     f = lib.mpq_linear_workspace_bytes
-    assert f(P, 8, P, 8, 4, 8, 8) == 0 and f(P, 9, P, 8, 1, 8, 8) == 0
-    assert f(P, 9, P, 9, 4, 8, 9) == 256 + 256 and f(C.c_void_p(4098), 8, P, 8, 4, 8, 8) == 256
-    assert f(P, 0, P, 8, 4, 8, 8) == 256  # rows that overlap
+    assert f(P, 8, P, 8, 6, 8, 8) == 0 and f(P, 9, P, 8, 2, 8, 8) == 0 and f(C.c_void_p(4098), 9, P, 9, 1, 8, 8) == 0
+    assert f(P, 9, P, 9, 6, 8, 9) == 256 + 256 and f(C.c_void_p(4098), 8, P, 8, 6, 8, 8) == 256
+    assert f(P, 0, P, 8, 6, 8, 8) == 256  # rows that overlap
     # too little of it, and off its boundary
-    assert linear(lib, ldx=9, ws=P, wsb=255) == 1 and linear(lib, ldx=9, ws=C.c_void_p(4100), wsb=4096) == 1
+    assert linear(lib, rows=6, ldx=9, ws=P, wsb=255) == 1
+    assert linear(lib, rows=6, ldx=9, ws=C.c_void_p(4100), wsb=4096) == 1
 
 
 def test_linear_backward_refuses(mpq):
