@@ -140,6 +140,27 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* tm, uint32_t bar, u
           : "memory");
   }
 }
+// One lane of a converged warp.  The MMA loops run in the whole warp, with the
+// issuing instructions alone in one lane, so that descriptors and counters stay
+// in uniform registers (moving them there cost 65 cycles per MMA).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// Whether a phase is complete (asked one stage ahead, while MMAs are issued)
+__device__ __forceinline__ bool mbar_done_cl(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // completion of the pair's MMAs issued so far, on the barrier at the same
 // place in both CTAs
 __device__ __forceinline__ void commit_both(uint64_t* bar) {
@@ -180,32 +201,40 @@ __device__ __forceinline__ void lin_residual(const LinOut& o, int row, int col, 
     load_edge<W>(static_cast<const O*>(o.residual) + (int64_t)row * o.ldr + col, r, o.cols - col, o.res_vec);
 }
 // One run of W consecutive columns of a row: bias, activation, residual, store.
-template <int W, typename T, typename O>
+// FEAT false: the bias at most.  FULL: the run lies within the matrix and on
+// aligned addresses.
+template <int W, typename T, typename O, bool FEAT = true, bool FULL = false>
 __device__ __forceinline__ void lin_finish(const LinOut& o, int row, int col, float (&v)[W],
                                            const float (&bias)[W], const float (&r)[W]) {
   const int n = o.cols - col;  // >= 1
   const int64_t at = (int64_t)row * o.ldo + col;
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias[i];
-  if (o.preact) store_edge<W>(static_cast<T*>(o.preact) + at, v, n, o.out_vec);
-  if (o.act != MPQ_ACT_NONE) {
+  if (FEAT) {
+    if (o.preact) {
+      if (FULL) store_vec<W>(static_cast<T*>(o.preact) + at, v, true);
+      else store_edge<W>(static_cast<T*>(o.preact) + at, v, n, o.out_vec);
+    }
+    if (o.act != MPQ_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = act_value(v[i], o.act);
-  }
-  if (o.residual) {
+      for (int i = 0; i < W; ++i) v[i] = act_value(v[i], o.act);
+    }
+    if (o.residual) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] += r[i];
+      for (int i = 0; i < W; ++i) v[i] += r[i];
+    }
   }
-  store_edge<W>(static_cast<O*>(o.out) + at, v, n, o.out_vec);
+  if (FULL) store_vec<W>(static_cast<O*>(o.out) + at, v, true);
+  else store_edge<W>(static_cast<O*>(o.out) + at, v, n, o.out_vec);
 }
 
 // ----------------------------------------------------------- CTA-pair GEMM --
 constexpr int PT = 256;                    // tile: 256 rows x 256 columns
-constexpr int P_STAGES = 6;
-constexpr int P_STAGE = 2 * 128 * BK * 2;  // 128 rows of A and 128 of B per CTA
+constexpr int P_RING = 6 * 2 * 128 * BK * 2;  // 6 stages of 128 rows of A and 128 of B per CTA,
+constexpr int P_STAGES = 8;                   // or 8 of 128 and 64 (128-column tiles only)
 constexpr int P_EPI = 8;                   // epilogue warps
 constexpr int P_THREADS = 32 * (3 + P_EPI);
-constexpr int P_SMEM = P_STAGES * P_STAGE + P_EPI * 4096 + 1024 + 256;
+constexpr int P_SMEM = P_RING + P_EPI * 4096 + 1024 + 256;
 static_assert(P_SMEM <= 232448, "pair kernel's shared memory");
 
 // The walk over tiles: whole waves of 256 x 256 tiles; what is left for a last
@@ -244,24 +273,25 @@ __device__ __forceinline__ void walk_tile(const Walk& w, int t, int& m0, int& n0
 // stage and descriptors built per MMA they took 450 and 540 cycles a stage, and
 // 600 with the waits.  So A and B have a copying warp each, a copy is as large
 // as a box may be, a commit reaches both CTAs, and descriptors are added up.
-template <typename T, typename O, bool A_MN, bool B_MN>
+template <typename T, typename O, bool A_MN, bool B_MN, bool FEAT>
 __global__ void __launch_bounds__(P_THREADS, 1)
     k_lin_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                const __grid_constant__ CUtensorMap tb_half, int KC, const __grid_constant__ LinOut o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* stg_all = smem + P_STAGES * P_STAGE;
+  uint8_t* stg_all = smem + P_RING;
   uint64_t* full = (uint64_t*)(stg_all + P_EPI * 4096);
   uint64_t* empty = full + P_STAGES;
   uint64_t* tm_full = empty + P_STAGES;
   uint64_t* tm_empty = tm_full + 2;
   uint32_t* tmem_slot = (uint32_t*)(tm_empty + 2);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // rank 0 issues the pair's MMAs
   const int worker = (int)cluster_id_x(), nworkers = (int)(gridDim.x / 2);
   const Walk walk = make_walk(o.rows, o.cols, nworkers);
   const int KT = (KC + BK - 1) / BK;
+  const int stages = walk.whole ? 6 : 8, stage = walk.whole ? P_RING / 6 : P_RING / 8;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < P_STAGES; ++s) {
@@ -313,14 +343,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           break;
         }
         const uint32_t fb = full_r0 + 8u * (uint32_t)s;  // rank 0's barrier counts both CTAs' bytes
-        uint8_t* dst = dst0 + s * P_STAGE;
+        uint8_t* dst = dst0 + s * stage;
         if (is_a) {
           if (rank == 0) mbar_expect_tx(&full[s], 2 * bytes);
           load_tile<A_MN, true>(&ta, fb, dst, r0, k0, 128);
         } else {
           load_tile<B_MN, true>(tm, fb, dst, r0, k0, wn / 2);
         }
-        if (++s == P_STAGES) {
+        if (++s == stages) {
           s = 0;
           phase ^= 1;
         }
@@ -329,48 +359,50 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     // every copy lands before the CTA leaves (rank 0's barriers count both
     // CTAs' copies; rank 1 waits for rank 0 at the closing cluster barrier)
     if (rank == 0)
-      for (uint32_t q = (it > (uint32_t)P_STAGES ? it - P_STAGES : 0); q < it; ++q)
-        for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&full[q % P_STAGES], (q / P_STAGES) & 1); ++i)
+      for (uint32_t q = (it > (uint32_t)stages ? it - stages : 0); q < it; ++q)
+        for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&full[q % stages], (q / stages) & 1); ++i)
           if (i > 256) __nanosleep(64);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t ID_W = lin_idesc<T, A_MN, B_MN>(256, PT), ID_N = lin_idesc<T, A_MN, B_MN>(256, PT / 2);
     const uint64_t da0 = op_desc<A_MN>(smem_u32(smem)), db0 = op_desc<B_MN>(smem_u32(smem) + 128 * BK * 2);
     uint32_t tl = 0;
     int s = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true, ready = false;
     for (int t = worker; t < walk.total && ok; t += nworkers, ++tl) {
       const int buf = tl & 1;
-      int m0, n0, wn;
-      walk_tile(walk, t, m0, n0, wn);
-      const uint32_t idesc = wn == PT ? ID_W : ID_N;
+      const uint32_t idesc = t < walk.whole ? ID_W : ID_N;
       if (tl >= 2 && !mbar_wait_cl(&tm_empty[buf], (tl / 2 - 1) & 1)) {
-        atomicOr(&g_lin_status, STATUS_TIMEOUT);
         ok = false;
         break;
       }
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)buf * PT;
       for (int kt = 0; kt < KT; ++kt) {
-        if (!mbar_wait_cl(&full[s], phase)) {
-          atomicOr(&g_lin_status, STATUS_TIMEOUT);
+        if (!ready && !mbar_wait_cl(&full[s], phase)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint64_t da = da0 + (uint32_t)s * (P_STAGE >> 4), db = db0 + (uint32_t)s * (P_STAGE >> 4);
-#pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          umma_f16_cg2(d, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (kt | kk) != 0 ? 1u : 0u);
-        commit_both(&empty[s]);
-        if (++s == P_STAGES) {
+        const uint64_t da = da0 + (uint32_t)s * (uint32_t)(stage >> 4), db = db0 + (uint32_t)s * (uint32_t)(stage >> 4);
+        uint64_t* freed = &empty[s];
+        if (++s == stages) {
           s = 0;
           phase ^= 1;
         }
+        ready = mbar_done_cl(&full[s], phase);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            umma_f16_cg2(d, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (kt | kk) != 0 ? 1u : 0u);
+          commit_both(freed);
+          if (kt == KT - 1) commit_both(&tm_full[buf]);
+        }
+        __syncwarp();
       }
-      if (ok) commit_both(&tm_full[buf]);
     }
+    if (!ok && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
     for (uint32_t q = (tl > 2 ? tl - 2 : 0); q < tl; ++q)  // MMAs finish before TMEM is freed
       for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&tm_full[q & 1], (q / 2) & 1); ++i)
         if (i > 256) __nanosleep(64);
@@ -397,6 +429,18 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       const int row0 = m0 + (int)rank * 128 + q * 32;
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)buf * PT;
       for (int c0 = side * 32; c0 < wn; c0 += 64) {
+        const int col = n0 + c0 + c8;
+        // this chunk lies within the matrix, on aligned addresses
+        const bool full_chunk = wide && row0 + 32 <= o.rows && n0 + c0 + 32 <= o.cols;
+        float bias[8] = {}, res[4][8];
+        if (full_chunk) {  // (in flight while the accumulator is read)
+          if (o.bias) load_param<8, T>(o.bias, o.bias_f32, col, bias, 8, o.bias_vec);
+          if (FEAT && o.residual) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              load_vec<8>(static_cast<const O*>(o.residual) + (int64_t)(row0 + i * 8 + r8) * o.ldr + col, res[i], true);
+          }
+        }
         uint32_t v[32];
         tmem_ld32(tbase + (uint32_t)c0, v);
         if (c0 + 64 >= wn) {  // this warp's part is read: hand the accumulator back
@@ -404,7 +448,6 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);
         }
-        const int col = n0 + c0 + c8;
         if (n0 + c0 >= o.cols) continue;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -412,41 +455,46 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
                           __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
         __syncwarp();
-        if (wide) {
-          float bias[8] = {};
+        if (full_chunk) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = i * 8 + r8;
+            const float4 x0 = stg[rr * 8 + ((c8 / 4) ^ (rr & 7))];
+            const float4 x1 = stg[rr * 8 + ((c8 / 4 + 1) ^ (rr & 7))];
+            float w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+            lin_finish<8, T, O, FEAT, true>(o, row0 + rr, col, w, bias, res[i]);
+          }
+        } else if (wide) {
           if (o.bias && col < o.cols)
             load_param<8, T>(o.bias, o.bias_f32, col, bias, o.cols - col, o.bias_vec);
-          if (col < o.cols) {
-            float res[4][8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (row0 + i * 8 + r8 < o.rows) lin_residual<8, O>(o, row0 + i * 8 + r8, col, res[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = i * 8 + r8;
-              if (row0 + rr < o.rows) {
-                const float4 x0 = stg[rr * 8 + ((c8 / 4) ^ (rr & 7))];
-                const float4 x1 = stg[rr * 8 + ((c8 / 4 + 1) ^ (rr & 7))];
-                float w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                lin_finish<8, T, O>(o, row0 + rr, col, w, bias, res[i]);
-              }
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int rr = i * 8 + r8;
+            if (col < o.cols && row0 + rr < o.rows) {
+              lin_residual<8, O>(o, row0 + rr, col, res[0]);
+              const float4 x0 = stg[rr * 8 + ((c8 / 4) ^ (rr & 7))];
+              const float4 x1 = stg[rr * 8 + ((c8 / 4 + 1) ^ (rr & 7))];
+              float w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+              lin_finish<8, T, O, FEAT>(o, row0 + rr, col, w, bias, res[0]);
             }
           }
         } else if (n0 + c0 + lane < o.cols) {  // unaligned rows: a column a lane
-          float bias[1] = {};
-          if (o.bias) load_param<1, T>(o.bias, o.bias_f32, n0 + c0 + lane, bias, 1, false);
+          float b1[1] = {};
+          if (o.bias) load_param<1, T>(o.bias, o.bias_f32, n0 + c0 + lane, b1, 1, false);
           const int top = min(32, o.rows - row0);
-          for (int r0 = 0; r0 < top; r0 += 16) {
-            float res[16][1];
+          for (int r0 = 0; r0 < top; r0 += 8) {
+            float r1[8][1];
+            if (FEAT) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (r0 + i < top) lin_residual<1, O>(o, row0 + r0 + i, n0 + c0 + lane, res[i]);
+              for (int i = 0; i < 8; ++i)
+                if (r0 + i < top) lin_residual<1, O>(o, row0 + r0 + i, n0 + c0 + lane, r1[i]);
+            }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const int rr = r0 + i;
               if (rr >= top) break;
               float w[1] = {reinterpret_cast<const float*>(stg + rr * 8 + ((lane >> 2) ^ (rr & 7)))[lane & 3]};
-              lin_finish<1, T, O>(o, row0 + rr, n0 + c0 + lane, w, bias, res[i]);
+              lin_finish<1, T, O, FEAT>(o, row0 + rr, n0 + c0 + lane, w, b1, r1[i]);
             }
           }
         }
@@ -497,7 +545,7 @@ __global__ void __launch_bounds__(S_THREADS)
   uint64_t* arrived = done + 1;  // S > 1: every CTA's part of this CTA's share is in recv
   uint32_t* tmem_slot = (uint32_t*)(arrived + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = g.S > 1 ? (int)cluster_ctarank() : 0;
   const int a0 = blockIdx.y * 128, b0 = blockIdx.z * g.NT;
   const int k_lo = (int)((int64_t)g.KT * rank / g.S), k_hi = (int)((int64_t)g.KT * (rank + 1) / g.S);
@@ -552,28 +600,35 @@ __global__ void __launch_bounds__(S_THREADS)
     for (int q = (i > g.stages ? i - g.stages : 0); q < i; ++q)  // every copy lands
       for (uint32_t w = 0; w < (1u << 25) && !mbar_try_wait(&full[q % g.stages], (q / g.stages) & 1); ++w)
         if (w > 256) __nanosleep(64);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     const uint32_t idesc = lin_idesc<T, A_MN, B_MN>(128, g.NT);
     const uint64_t da0 = op_desc<A_MN>(smem_u32(smem)), db0 = op_desc<B_MN>(smem_u32(smem) + 128 * BK * 2);
     int s = 0;
     uint32_t phase = 0;
+    bool ready = false;
     for (int i = 0; i < nk; ++i) {
-      if (!mbar_wait(&full[s], phase)) {
-        atomicOr(&g_lin_status, STATUS_TIMEOUT);
+      if (!ready && !mbar_wait(&full[s], phase)) {
+        if (lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
         break;
       }
       tc_fence_after();
       const uint64_t da = da0 + (uint32_t)s * (uint32_t)(stage >> 4), db = db0 + (uint32_t)s * (uint32_t)(stage >> 4);
-#pragma unroll
-      for (int kk = 0; kk < BK / 16; ++kk)
-        umma_f16(tmem, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (i | kk) != 0 ? 1u : 0u);
-      umma_commit(&empty[s]);
+      uint64_t* freed = &empty[s];
       if (++s == g.stages) {
         s = 0;
         phase ^= 1;
       }
+      ready = mbar_test_wait(&full[s], phase);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          umma_f16(tmem, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (i | kk) != 0 ? 1u : 0u);
+        umma_commit(freed);
+      }
+      __syncwarp();
     }
-    umma_commit(done);
+    if (elect_one()) umma_commit(done);
+    __syncwarp();
     for (uint32_t w = 0; w < (1u << 25) && !mbar_try_wait(done, 0); ++w)
       if (w > 256) __nanosleep(64);
   } else if (warp >= 2) {
@@ -902,7 +957,9 @@ mpq_status pack(Operand* a, void* dst_a, Operand* b, void* dst_b, cudaStream_t s
 
 template <typename T, typename O, bool RN, bool CN>
 mpq_status set_attrs() {
-  MPQ_CUDA(cudaFuncSetAttribute(k_lin_pair<T, O, RN, CN>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
+  MPQ_CUDA(cudaFuncSetAttribute(k_lin_pair<T, O, RN, CN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
+  if constexpr (!RN && !CN)
+    MPQ_CUDA(cudaFuncSetAttribute(k_lin_pair<T, O, RN, CN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
   MPQ_CUDA(cudaFuncSetAttribute(k_lin_split<T, O, CN, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 220 * 1024));
   return MPQ_OK;
@@ -943,7 +1000,7 @@ mpq_status lin_device(int* dev_out, int* sms_out) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int nc = 0;
-    if (cudaOccupancyMaxActiveClusters(&nc, k_lin_pair<B, B, false, false>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&nc, k_lin_pair<B, B, false, false, true>, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       nc = 0;
     }
@@ -985,7 +1042,10 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    MPQ_CUDA(cudaLaunchKernelEx(&cfg, k_lin_pair<T, O, RN, CN>, ta, tb, tb_half, (int)KC, o));
+    auto kern = k_lin_pair<T, O, RN, CN, false>;
+    if constexpr (!RN && !CN)
+      if (o.act != MPQ_ACT_NONE || o.residual || o.preact) kern = k_lin_pair<T, O, RN, CN, true>;
+    MPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, ta, tb, tb_half, (int)KC, o));
   } else {
     SplitGeom g;
     g.NT = RN ? (o.rows <= 64 ? 64 : 128) : (int)std::min<int64_t>(128, round_up(o.rows, 16));
