@@ -14,7 +14,6 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "f32x2.cuh"
 #include "layer_ops.cuh"
 
 namespace mpq {
@@ -132,29 +131,6 @@ __device__ __forceinline__ void ln_param(const LnArgs& a, const void* p, float d
   }
 }
 
-// 8 elements as 4 packed pairs
-struct F8 {
-  uint64_t p[4];
-};
-template <typename T>
-__device__ __forceinline__ F8 pairs(const Raw8<T>& r) {
-  float v[8];
-  decode<T>(r, v);
-  F8 f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
-  return f;
-}
-__device__ __forceinline__ F8 pairs(const float (&v)[8]) {
-  F8 f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
-  return f;
-}
-__device__ __forceinline__ void unpairs(const F8& f, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f2_unpack(f.p[i], v[2 * i], v[2 * i + 1]);
-}
 __device__ __forceinline__ float f2_sum(uint64_t a) {
   float x, y;
   f2_unpack(a, x, y);

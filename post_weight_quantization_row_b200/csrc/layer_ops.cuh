@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "f32x2.cuh"
 #include "mpq_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -151,6 +152,29 @@ __device__ __forceinline__ void decode(const Raw8<T>& r, float (&x)[8]) {
       x[2 * i + 1] = f.y;
     }
   }
+}
+// 8 elements as 4 packed pairs
+struct F8 {
+  uint64_t p[4];
+};
+template <typename T>
+__device__ __forceinline__ F8 pairs(const Raw8<T>& r) {
+  float v[8];
+  decode<T>(r, v);
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+  return f;
+}
+__device__ __forceinline__ F8 pairs(const float (&v)[8]) {
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+  return f;
+}
+__device__ __forceinline__ void unpairs(const F8& f, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(f.p[i], v[2 * i], v[2 * i + 1]);
 }
 // The first n of 8 elements (all for n >= 8, none for n <= 0), the others 0;
 // vec: the address is on a 16-byte boundary.

@@ -24,7 +24,6 @@
 #include <algorithm>
 #include <mutex>
 
-#include "f32x2.cuh"
 #include "layer_ops.cuh"
 
 namespace mpq {
@@ -49,17 +48,15 @@ constexpr float LOG2E = 1.4426950408889634f;
 // squares for the least relative error (1.2e-7; in fp32 2.2e-7 absolute, and
 // 1.4e-6 relative up to a = 5, from the rounding of the exponent).
 // Half the instructions of erfcf and expf.
+__device__ constexpr float TAIL[8] = {0.11962516605854034f, 0.12081687152385712f,  0.09952317178249359f,
+                                      0.1298430860042572f,  -0.05609530583024025f, 0.2089640498161316f,
+                                      -0.15871335566043854f, 0.03603625297546387f};
 __device__ __forceinline__ float normal_tail(float a, float& e) {
   e = ex2(-0.5f * LOG2E * a * a);
   const float t = rcp_approx(fmaf(0.3f, a, 1.0f));
-  float q = 0.03603625297546387f;
-  q = fmaf(q, t, -0.15871335566043854f);
-  q = fmaf(q, t, 0.2089640498161316f);
-  q = fmaf(q, t, -0.05609530583024025f);
-  q = fmaf(q, t, 0.1298430860042572f);
-  q = fmaf(q, t, 0.09952317178249359f);
-  q = fmaf(q, t, 0.12081687152385712f);
-  q = fmaf(q, t, 0.11962516605854034f);
+  float q = TAIL[7];
+#pragma unroll
+  for (int i = 6; i >= 0; --i) q = fmaf(q, t, TAIL[i]);
   return q * t * e;
 }
 __device__ __forceinline__ float act_value(float z, int act) {
@@ -99,6 +96,88 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   const float e = ex2(-LOG2E * fabsf(u)), d = rcp_approx(1.0f + e);
   const float s = u >= 0.0f ? d : e * d;  // 1/(1 + e^-u)
   return fmaf(c * (e * d * d), du, s);    // s + c s (1 - s) u'
+}
+
+// normal_tail of two values: Q = Phi(-a) / e, e = e^(-a^2/2)
+__device__ __forceinline__ uint64_t f2_both(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ void normal_tail2(uint64_t a, uint64_t& q, uint64_t& e) {
+  float x0, x1;
+  f2_unpack(f2_mul(f2_mul(a, f2_both(-0.5f * LOG2E)), a), x0, x1);
+  e = f2_pack(ex2(x0), ex2(x1));
+  f2_unpack(f2_fma(a, f2_both(0.3f), f2_both(1.0f)), x0, x1);
+  const uint64_t t = f2_pack(rcp_approx(x0), rcp_approx(x1));
+  q = f2_both(TAIL[7]);
+#pragma unroll
+  for (int i = 6; i >= 0; --i) q = f2_fma(q, t, f2_both(TAIL[i]));
+  q = f2_mul(q, t);
+}
+// The activation of N values: one choice for all, so that its code is there
+// once.
+template <int N>
+__device__ __forceinline__ void act_apply(float (&v)[N], int act) {
+  switch (act) {
+    case MPQ_ACT_GELU:
+      if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {  // z Phi(z) with u = z Phi(-|z|): z - u for z >= 0, u below
+          const uint64_t z = f2_pack(v[i], v[i + 1]);
+          uint64_t q, e;
+          normal_tail2(f2_pack(fabsf(v[i]), fabsf(v[i + 1])), q, e);
+          const uint64_t u = f2_mul(f2_mul(q, e), z);
+          float u0, u1, w0, w1;
+          f2_unpack(u, u0, u1);
+          f2_unpack(f2_sub(z, u), w0, w1);
+          v[i] = v[i] >= 0.0f ? w0 : u0;
+          v[i + 1] = v[i + 1] >= 0.0f ? w1 : u1;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = act_value(v[i], MPQ_ACT_GELU);
+      }
+      return;
+    case MPQ_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_value(v[i], MPQ_ACT_RELU);
+      return;
+    case MPQ_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_value(v[i], MPQ_ACT_GELU_TANH);
+      return;
+    case MPQ_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_value(v[i], MPQ_ACT_SILU);
+      return;
+    default: return;
+  }
+}
+// dy * act'(z) of 8 elements.  gelu on packed pairs: with a = |z| and w =
+// Phi(-a) - a phi(a), act'(z) is 1 - w for z >= 0 and w below.
+__device__ __forceinline__ void act_grad8(F8& g, const F8& z, int act) {
+  if (act == MPQ_ACT_NONE) return;
+  if (act != MPQ_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float z0, z1;
+      f2_unpack(z.p[i], z0, z1);
+      g.p[i] = f2_mul(g.p[i], f2_pack(act_slope(z0, act), act_slope(z1, act)));
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float z0, z1, a0, a1;
+    f2_unpack(z.p[i], z0, z1);
+    asm("min.NaN.f32 %0, %1, 0f41F00000;" : "=f"(a0) : "f"(fabsf(z0)));  // 30: w is 0 from there on
+    asm("min.NaN.f32 %0, %1, 0f41F00000;" : "=f"(a1) : "f"(fabsf(z1)));
+    const uint64_t a = f2_pack(a0, a1);
+    uint64_t q, e;
+    normal_tail2(a, q, e);
+    const uint64_t w = f2_mul(f2_fma(a, f2_both(-0.3989422804014327f), q), e);
+    float w0, w1, v0, v1;
+    f2_unpack(w, w0, w1);
+    f2_unpack(f2_sub(f2_both(1.0f), w), v0, v1);
+    g.p[i] = f2_mul(g.p[i], f2_pack(z0 >= 0.0f ? v0 : w0, z1 >= 0.0f ? v1 : w1));
+  }
 }
 
 // ------------------------------------------------------------- the operand --
@@ -201,31 +280,20 @@ __device__ __forceinline__ void lin_residual(const LinOut& o, int row, int col, 
     load_edge<W>(static_cast<const O*>(o.residual) + (int64_t)row * o.ldr + col, r, o.cols - col, o.res_vec);
 }
 // One run of W consecutive columns of a row: bias, activation, residual, store.
-// FEAT false: the bias at most.  FULL: the run lies within the matrix and on
-// aligned addresses.
-template <int W, typename T, typename O, bool FEAT = true, bool FULL = false>
+template <int W, typename T, typename O>
 __device__ __forceinline__ void lin_finish(const LinOut& o, int row, int col, float (&v)[W],
                                            const float (&bias)[W], const float (&r)[W]) {
   const int n = o.cols - col;  // >= 1
   const int64_t at = (int64_t)row * o.ldo + col;
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias[i];
-  if (FEAT) {
-    if (o.preact) {
-      if (FULL) store_vec<W>(static_cast<T*>(o.preact) + at, v, true);
-      else store_edge<W>(static_cast<T*>(o.preact) + at, v, n, o.out_vec);
-    }
-    if (o.act != MPQ_ACT_NONE) {
+  if (o.preact) store_edge<W>(static_cast<T*>(o.preact) + at, v, n, o.out_vec);
+  if (o.act != MPQ_ACT_NONE) act_apply<W>(v, o.act);
+  if (o.residual) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = act_value(v[i], o.act);
-    }
-    if (o.residual) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] += r[i];
-    }
+    for (int i = 0; i < W; ++i) v[i] += r[i];
   }
-  if (FULL) store_vec<W>(static_cast<O*>(o.out) + at, v, true);
-  else store_edge<W>(static_cast<O*>(o.out) + at, v, n, o.out_vec);
+  store_edge<W>(static_cast<O*>(o.out) + at, v, n, o.out_vec);
 }
 
 // ----------------------------------------------------------- CTA-pair GEMM --
@@ -418,27 +486,37 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint32_t tl = 0;
     for (int t = worker; t < walk.total; t += nworkers, ++tl) {
       const int buf = tl & 1;
+      int m0, n0, wn;
+      walk_tile(walk, t, m0, n0, wn);
+      const int row0 = m0 + (int)rank * 128 + q * 32;
+      if (FEAT && o.residual && row0 + lane < o.rows) {  // this warp's residual comes to L2 during the MMAs
+        const O* rl = static_cast<const O*>(o.residual) + (int64_t)(row0 + lane) * o.ldr;
+        for (int c = n0 + side * 32; c < min(n0 + wn, o.cols); c += 64) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(rl + c));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(rl + min(c + 31, o.cols - 1)));
+        }
+      }
       const bool ok = __all_sync(0xffffffffu, mbar_wait_cl(&tm_full[buf], (tl / 2) & 1));
       if (!ok) {
         if (lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
         break;
       }
       tc_fence_after();
-      int m0, n0, wn;
-      walk_tile(walk, t, m0, n0, wn);
-      const int row0 = m0 + (int)rank * 128 + q * 32;
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)buf * PT;
       for (int c0 = side * 32; c0 < wn; c0 += 64) {
-        const int col = n0 + c0 + c8;
-        // this chunk lies within the matrix, on aligned addresses
-        const bool full_chunk = wide && row0 + 32 <= o.rows && n0 + c0 + 32 <= o.cols;
-        float bias[8] = {}, res[4][8];
-        if (full_chunk) {  // (in flight while the accumulator is read)
-          if (o.bias) load_param<8, T>(o.bias, o.bias_f32, col, bias, 8, o.bias_vec);
-          if (FEAT && o.residual) {
+        const int left = o.cols - (n0 + c0), top = o.rows - row0;  // columns and rows from this chunk on
+        const bool inside = wide && left >= 32 && top >= 32;
+        // bias and residual in the layout of the stores, in flight while the
+        // accumulator is read
+        float bias[8] = {};
+        Raw8<O> res[4] = {};
+        const bool has_res = FEAT && o.residual;
+        const O* rp = static_cast<const O*>(o.residual) + (int64_t)row0 * o.ldr + n0 + c0;
+        if (inside) {
+          if (o.bias) load_param<8, T>(o.bias, o.bias_f32, n0 + c0 + c8, bias, 8, o.bias_vec);
+          if (has_res) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              load_vec<8>(static_cast<const O*>(o.residual) + (int64_t)(row0 + i * 8 + r8) * o.ldr + col, res[i], true);
+            for (int i = 0; i < 4; ++i) res[i] = load_raw<O>(rp + (int64_t)(i * 8 + r8) * o.ldr + c8, 8, true);
           }
         }
         uint32_t v[32];
@@ -448,53 +526,67 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);
         }
-        if (n0 + c0 >= o.cols) continue;
+        if (left <= 0 || top <= 0) continue;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           stg[lane * 8 + (k ^ (lane & 7))] =
               make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
                           __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
         __syncwarp();
-        if (full_chunk) {
-#pragma unroll
+        // rolled loops: a tile's epilogue runs its code once or a few times,
+        // and its length is paid in instruction fetches
+        if (inside) {
+          const int64_t at0 = (int64_t)(row0 + r8) * o.ldo + n0 + c0 + c8;
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             const int rr = i * 8 + r8;
             const float4 x0 = stg[rr * 8 + ((c8 / 4) ^ (rr & 7))];
             const float4 x1 = stg[rr * 8 + ((c8 / 4 + 1) ^ (rr & 7))];
             float w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-            lin_finish<8, T, O, FEAT, true>(o, row0 + rr, col, w, bias, res[i]);
-          }
-        } else if (wide) {
-          if (o.bias && col < o.cols)
-            load_param<8, T>(o.bias, o.bias_f32, col, bias, o.cols - col, o.bias_vec);
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int rr = i * 8 + r8;
-            if (col < o.cols && row0 + rr < o.rows) {
-              lin_residual<8, O>(o, row0 + rr, col, res[0]);
-              const float4 x0 = stg[rr * 8 + ((c8 / 4) ^ (rr & 7))];
-              const float4 x1 = stg[rr * 8 + ((c8 / 4 + 1) ^ (rr & 7))];
-              float w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-              lin_finish<8, T, O, FEAT>(o, row0 + rr, col, w, bias, res[0]);
-            }
-          }
-        } else if (n0 + c0 + lane < o.cols) {  // unaligned rows: a column a lane
-          float b1[1] = {};
-          if (o.bias) load_param<1, T>(o.bias, o.bias_f32, n0 + c0 + lane, b1, 1, false);
-          const int top = min(32, o.rows - row0);
-          for (int r0 = 0; r0 < top; r0 += 8) {
-            float r1[8][1];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] += bias[j];
+            const int64_t at = at0 + (int64_t)(i * 8) * o.ldo;
             if (FEAT) {
+              if (o.preact) store_vec<8>(static_cast<T*>(o.preact) + at, w, true);
+              if (o.act != MPQ_ACT_NONE) act_apply<8>(w, o.act);
+              if (has_res) {
+                float r[8];
+                decode<O>(i == 0 ? res[0] : i == 1 ? res[1] : i == 2 ? res[2] : res[3], r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] += r[j];
+              }
+            }
+            store_vec<8>(static_cast<O*>(o.out) + at, w, true);
+          }
+        } else if (lane < left) {
+          // edges and unaligned rows: a column a lane, 8 rows at a time, the
+          // residual of the next 8 in flight
+          const int64_t at0 = (int64_t)row0 * o.ldo + n0 + c0 + lane;
+          float b1[1] = {}, r0[8] = {}, r1[8] = {};
+          if (o.bias) load_param<1, T>(o.bias, o.bias_f32, n0 + c0 + lane, b1, 1, false);
+          if (has_res) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < top) r0[i] = to_f(rp[(int64_t)i * o.ldr + lane]);
+          }
+#pragma unroll 1
+          for (int q = 0; q < min(32, top); q += 8) {
+            if (has_res) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (r0 + i < top) lin_residual<1, O>(o, row0 + r0 + i, n0 + c0 + lane, r1[i]);
+                if (q < 24 && q + 8 + i < top) r1[i] = to_f(rp[(int64_t)(q + 8 + i) * o.ldr + lane]);
             }
+            float w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int rr = r0 + i;
-              if (rr >= top) break;
-              float w[1] = {reinterpret_cast<const float*>(stg + rr * 8 + ((lane >> 2) ^ (rr & 7)))[lane & 3]};
-              lin_finish<1, T, O, FEAT>(o, row0 + rr, n0 + c0 + lane, w, b1, r1[i]);
+              w[i] = reinterpret_cast<const float*>(stg + (q + i) * 8 + ((lane >> 2) ^ i))[lane & 3] + b1[0];
+              if (FEAT && o.preact && q + i < top) static_cast<T*>(o.preact)[at0 + (int64_t)(q + i) * o.ldo] = from_f<T>(w[i]);
+            }
+            if (FEAT && o.act != MPQ_ACT_NONE) act_apply<8>(w, o.act);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (q + i < top) static_cast<O*>(o.out)[at0 + (int64_t)(q + i) * o.ldo] = from_f<O>(w[i] + r0[i]);
+              r0[i] = r1[i];
             }
           }
         }
@@ -831,7 +923,7 @@ __global__ void __launch_bounds__(256)
   const int cg = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.y * 256 + cg * 8;
   const int64_t r_lo = (int64_t)blockIdx.x * DZ_ROWS, r_hi = min(rows, r_lo + DZ_ROWS);
-  float sum[8] = {};
+  F8 sum = {};
   if (c < n) {
     const int left = (int)min((int64_t)8, n - c);
     constexpr int NR = 4;  // rows in flight
@@ -848,23 +940,23 @@ __global__ void __launch_bounds__(256)
       for (int q = 0; q < NR; ++q) {
         const int64_t r = r0 + 8 * q;
         if (r >= r_hi) break;
-        float g[8];
-        decode<T>(gy[q], g);
-        if (act != MPQ_ACT_NONE) {
-          float u[8];
-          decode<T>(zz[q], u);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] *= act_slope(u[j], act);
+        F8 g = pairs<T>(gy[q]);
+        if (act != MPQ_ACT_NONE) act_grad8(g, pairs<T>(zz[q]), act);
+        if (dz) {  // ldd is a multiple of 8: the pad is zero
+          float v[8];
+          unpairs(g, v);
+          store_vec<8>(dz + r * ldd + c, v, true);
         }
-        if (dz) store_vec<8>(dz + r * ldd + c, g, true);  // ldd is a multiple of 8: the pad is zero
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += g[j];
+        for (int j = 0; j < 4; ++j) sum.p[j] = f2_add(sum.p[j], g.p[j]);
       }
     }
   }
   if (!part) return;
+  float total[8];
+  unpairs(sum, total);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) red[rl][cg * 8 + j] = sum[j];
+  for (int j = 0; j < 8; ++j) red[rl][cg * 8 + j] = total[j];
   __syncthreads();
   const int64_t col = (int64_t)blockIdx.y * 256 + threadIdx.x;
   if (col < n) {
