@@ -1103,6 +1103,41 @@ mpq_status lin_device(int* dev_out, int* sms_out) {
   return MPQ_OK;
 }
 
+// Geometry of the split kernel.  Tiles of up to 32 rows leave room for two
+// CTAs on an SM; the contraction is split while that finds free SMs and each
+// CTA keeps 4 steps.  Clusters of 8 only where they leave half of the SMs
+// free: 16 of them (256 x 1024 over 2048) find no place at once and take 18.7
+// us, clusters of 4 11.0.
+SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms) {
+  SplitGeom g{};
+  g.NT = rows_mn ? (o.rows <= 64 ? 64 : 128) : (int)std::min<int64_t>(128, round_up(o.rows, 16));
+  const int64_t tiles = cdiv(o.cols, 128) * cdiv(o.rows, g.NT);
+  const int per_sm = g.NT <= 32 ? 2 : 1;
+  g.S = 1;
+  while (g.S < 4 && tiles * g.S * 2 <= per_sm * sms && KT >= 4 * g.S) g.S *= 2;
+  if (g.S == 4 && tiles * 8 <= sms / 2 && KT >= 16) g.S = 8;
+  g.KT = (int)KT;
+  const int budget = 216 * 1024 / per_sm - split_recv_bytes(g.NT, g.S);
+  g.stages = (int)std::min<int64_t>(std::min(budget / split_stage_bytes(g.NT), 12), std::max<int64_t>(cdiv(KT, g.S), 1));
+  // the ring must also hold the partial tile
+  g.stages = std::max(g.stages, (int)cdiv(round_up(g.NT, 32) * 128 * 4, split_stage_bytes(g.NT)));
+  g.tmem_cols = 32;
+  while ((int)g.tmem_cols < g.NT) g.tmem_cols *= 2;
+  return g;
+}
+// What the two kernels take, in microseconds, fitted to 90 shapes of 130 to
+// 2560 rows, 128 to 4096 columns and contractions of 512 to 8192 (within 15%
+// where the two are near each other): a fixed part (launch, first copies, last
+// epilogue) and a part per step of 64.  256 x 512 over 2048: pair 11.7, split
+// 10.9; over 8192: 27.9 and 15.6; 1280 x 1024 over 8192: 29.9 and 35.3.
+double pair_us(const LinOut& o, int64_t KT, int pairs) {
+  const Walk w = make_walk(o.rows, o.cols, (int)std::min<int64_t>(2 * cdiv(o.rows, PT) * cdiv(o.cols, PT), pairs));
+  return 6.2 + (double)KT * (0.33 * (double)cdiv(w.whole, pairs) + 0.17 * (double)cdiv(w.total - w.whole, pairs));
+}
+double split_us(int64_t tiles, const SplitGeom& g, int sms) {
+  return 8.8 + 0.21 * (double)(cdiv(tiles * g.S, sms) * cdiv(g.KT, g.S));
+}
+
 // out[rows x cols] = R C^T over KC, the epilogue as `o` says.  RN / CN: the
 // operand that gives the output's rows / columns is stored with that index
 // contiguous (else with the contraction contiguous).
@@ -1115,9 +1150,10 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
   const int64_t KT = cdiv(KC, BK);
   const int64_t big = cdiv(o.rows, PT) * cdiv(o.cols, PT);
   const int pairs = g_lin_dev[dev].pairs;
+  const SplitGeom g = split_geom(o, RN, KT, sms);
+  const int64_t at_ = cdiv(o.cols, 128), bt = cdiv(o.rows, g.NT);
   ProfScope ps_(tag, st);
-  static const int LP = getenv("LP") ? atoi(getenv("LP")) : 1;
-  if (pairs > 0 && o.rows > 128 && big * 2 >= LP) {
+  if (pairs > 0 && o.rows > 128 && (bt > 65535 || pair_us(o, KT, pairs) <= split_us(at_ * bt, g, sms))) {
     CUtensorMap ta, tb, tb_half;
     MPQ_TRY(encode_box(&ta, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : 128));
     MPQ_TRY(encode_box(&tb, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
@@ -1139,21 +1175,7 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
       if (o.act != MPQ_ACT_NONE || o.residual || o.preact) kern = k_lin_pair<T, O, RN, CN, true>;
     MPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, ta, tb, tb_half, (int)KC, o));
   } else {
-    SplitGeom g;
-    g.NT = RN ? (o.rows <= 64 ? 64 : 128) : (int)std::min<int64_t>(128, round_up(o.rows, 16));
-    const int64_t at_ = cdiv(o.cols, 128), bt = cdiv(o.rows, g.NT);
     if (bt > 65535 || at_ > 65535) return fail(MPQ_ERR_INVALID_ARG, "linear: too many tiles");
-    static const int LS = getenv("LS") ? atoi(getenv("LS")) : 4;
-    const int per_sm = g.NT <= 32 ? 2 : 1;
-    g.S = 1;
-    while (g.S < LS && at_ * bt * g.S * 2 <= per_sm * sms && KT >= 4 * g.S) g.S *= 2;
-    g.KT = (int)KT;
-    const int budget = 216 * 1024 / per_sm - split_recv_bytes(g.NT, g.S);
-    g.stages = (int)std::min<int64_t>(std::min(budget / split_stage_bytes(g.NT), 12), std::max<int64_t>(cdiv(KT, g.S), 1));
-    // the ring must also hold the partial tile
-    g.stages = std::max(g.stages, (int)cdiv(round_up(g.NT, 32) * 128 * 4, split_stage_bytes(g.NT)));
-    g.tmem_cols = 32;
-    while ((int)g.tmem_cols < g.NT) g.tmem_cols *= 2;
     const int smem = g.stages * split_stage_bytes(g.NT) + split_recv_bytes(g.NT, g.S) + (2 * g.stages + 2) * 8 + 16 + 1024;
     CUtensorMap ta, tb;
     MPQ_TRY(encode_box(&ta, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
