@@ -14,22 +14,21 @@
 // Top alternatives without a second pass: every thread keeps the largest
 // logit it met.  The top-th largest of the maxima of 128 disjoint sets of
 // columns is a lower bound of the row's top-th largest logit, and only
-// threads whose maximum reaches it can hold a candidate (about `top` of 512),
+// threads whose maximum reaches it can hold a candidate (about `top` of 256),
 // so only their columns are read again, from L2.  The candidates are ranked
 // by counting.  The order is (logit descending, id ascending) throughout: a
 // total order, so the result does not depend on the order of any atomics.
 #include <algorithm>
 #include <type_traits>
 
-#include "f32x2.cuh"
 #include "layer_ops.cuh"
 
 namespace mpq {
 namespace {
 
-constexpr int AT = 512;            // threads per CTA
 constexpr int TOP_SETS = 128;      // sets of columns whose maxima bound the top list
 constexpr int CAND = 4096;         // candidates ranked at once
+constexpr int64_t L2_ROWS = 96ll << 20;  // logits at work that L2 (126 MB) is trusted with
 constexpr float M_FLOOR = -1e37f;  // start of the running maximum (scaled)
 constexpr float LN2 = 0.69314718055994531f, LOG2E = 1.4426950408889634f;
 static_assert(TOP_SETS >= MPQ_TOP_MAX, "a bound needs `top` sets");
@@ -111,10 +110,12 @@ __device__ __forceinline__ uint64_t full_key(float x, uint32_t id) {
 // One pass over vectors [lo, hi) of the row: the running softmax, and (TOP)
 // the thread's largest logit with its vector.  `best_g` stays -1 where no
 // logit above -inf was met.
-template <typename T, bool ENT, bool TOP>
+template <int AT, typename T, bool ENT, bool TOP>
 __device__ __forceinline__ Soft scan_row(const Row<T>& row, int lo, int hi, float k, float& best, int& best_g) {
   constexpr int U = sizeof(T) == 4 ? 2 : 4;  // 64 bytes in flight per thread
-  Soft a{M_FLOOR, 0.0f, 0.0f};
+  float m = M_FLOOR;
+  uint64_t s2 = 0ull, u2 = 0ull;
+  const uint64_t k2 = f2_pack(k, k);
   best = -INFINITY;
   best_g = -1;
   for (int g0 = lo + (int)threadIdx.x; g0 < hi; g0 += AT * U) {
@@ -132,22 +133,39 @@ __device__ __forceinline__ Soft scan_row(const Row<T>& row, int lo, int hi, floa
         best = top;
         best_g = g0 + j * AT;
       }
-      const float m = fmaxf(a.m, top * k);
-      const float d = a.m - m, c = ex2(d);
-      if (ENT) a.u = c * fmaf(d, a.s, a.u);
-      a.s *= c;
-      a.m = m;
+      const float old = m;
+      m = fmaxf(m, top * k);
+      const float d = old - m, c = ex2(d);
+      const uint64_t c2 = f2_pack(c, c);
+      if (ENT) u2 = f2_mul(c2, f2_fma(f2_pack(d, d), s2, u2));
+      s2 = f2_mul(s2, c2);
+      const uint64_t m2 = f2_pack(-m, -m);
+      float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // 2^-150 is 0 here, and keeps 0 * (-inf) out of the entropy's sum
-        float y = fmaf(x[i], k, -m);
-        if (ENT) y = max_nan(y, -150.0f);
-        const float e = ex2(y);
-        a.s += e;
-        if (ENT) a.u = fmaf(y, e, a.u);
+      for (int i = 0; i < 4; ++i) f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), k2, m2), y[2 * i], y[2 * i + 1]);
+      if (ENT) {
+        // masked logits: 2^-150 is 0 here, and keeps 0 * (-inf) out of the
+        // entropy's sum
+        const float low = fmin3(fmin3(fmin3(y[0], y[1], y[2]), y[3], y[4]), fminf(y[5], y[6]), y[7]);
+        if (low < -150.0f) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = max_nan(y[i], -150.0f);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t e2 = f2_pack(ex2(y[2 * i]), ex2(y[2 * i + 1]));
+        s2 = f2_add(s2, e2);
+        if (ENT) u2 = f2_fma(f2_pack(y[2 * i], y[2 * i + 1]), e2, u2);
       }
     }
   }
+  Soft a{m, 0.0f, 0.0f};
+  float e0, e1;
+  f2_unpack(s2, e0, e1);
+  a.s = e0 + e1;
+  f2_unpack(u2, e0, e1);
+  a.u = e0 + e1;
   return a;
 }
 
@@ -159,6 +177,7 @@ struct RowStat {
   bool empty;   // all are -inf
 };
 
+template <int AT>
 struct AnsShared {
   Soft warp[AT / 32];
   Soft cta;               // this CTA's part of the row (read by the cluster)
@@ -185,8 +204,8 @@ __device__ __forceinline__ uint64_t ld_cluster64(const uint64_t* p, int rank) {
 // thread gets the row's.  Rows whose logits all lie below the floor are
 // counted here: the spacing of fp32 there is so wide that a logit either
 // equals the largest or has probability 0.
-template <typename T, bool ENT, bool CL>
-__device__ __forceinline__ RowStat join_row(const Row<T>& row, int lo, int hi, Soft a, int C, AnsShared& sh) {
+template <int AT, typename T, bool ENT, bool CL>
+__device__ __forceinline__ RowStat join_row(const Row<T>& row, int lo, int hi, Soft a, int C, AnsShared<AT>& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   a = warp_merge<ENT>(a);
   if (lane == 0) sh.warp[warp] = a;
@@ -200,14 +219,13 @@ __device__ __forceinline__ RowStat join_row(const Row<T>& row, int lo, int hi, S
   sync_row<CL>();
   RowStat st;
   if (CL) {
-    st.a = Soft{M_FLOOR, 0.0f, 0.0f};
-    for (int r = 0; r < C; ++r) {
-      Soft b;
-      b.m = ld_cluster(&sh.cta.m, r);
-      b.s = ld_cluster(&sh.cta.s, r);
-      b.u = ENT ? ld_cluster(&sh.cta.u, r) : 0.0f;
-      st.a = merge<ENT>(st.a, b);
+    Soft b{M_FLOOR, 0.0f, 0.0f};
+    if (lane < C) {  // a lane per CTA, so that the remote loads overlap
+      b.m = ld_cluster(&sh.cta.m, lane);
+      b.s = ld_cluster(&sh.cta.s, lane);
+      b.u = ENT ? ld_cluster(&sh.cta.u, lane) : 0.0f;
     }
+    st.a = warp_merge<ENT>(b);
   } else {
     st.a = sh.cta;
   }
@@ -271,6 +289,7 @@ __device__ __forceinline__ float log_prob(const RowStat& st, float x, float k, f
 }
 
 // ---------------------------------------------------------- token_logprobs --
+template <int AT>
 struct TopShared {
   uint64_t sets[TOP_SETS];
   uint64_t cand[CAND];
@@ -284,20 +303,21 @@ struct TopShared {
 // Hands the `top` largest of n <= CAND keys to put(position, key), zeros
 // behind the last.  Few keys are ranked by counting; many are sorted
 // (bitonic; the buffer is padded to a power of two).
-template <typename F>
+template <int AT, typename F>
 __device__ __forceinline__ void rank_keys(uint64_t* keys, int n, int top, F put) {
   const int tid = threadIdx.x;
-  if (n <= TOP_SETS) {
+  if (n <= 2 * TOP_SETS) {
     for (int i = tid; i < n; i += AT) {
       const uint64_t key = keys[i];
       int rank = 0;
+#pragma unroll 8
       for (int j = 0; j < n; ++j) rank += (keys[j] > key || (keys[j] == key && j < i)) ? 1 : 0;
       if (rank < top) put(rank, key);
     }
     for (int i = n + tid; i < top; i += AT) put(i, 0ull);
     return;
   }
-  int p = 2 * TOP_SETS;
+  int p = 4 * TOP_SETS;
   while (p < n) p *= 2;
   for (int i = n + tid; i < p; i += AT) keys[i] = 0;
   __syncthreads();
@@ -314,24 +334,24 @@ __device__ __forceinline__ void rank_keys(uint64_t* keys, int n, int top, F put)
       }
       __syncthreads();
     }
-  for (int i = tid; i < top; i += AT) put(i, keys[i]);  // p >= 2 TOP_SETS > top
+  for (int i = tid; i < top; i += AT) put(i, keys[i]);  // p > top
 }
 
 // The CTA's `top` largest (logit, id) of vectors [lo, hi) into sh.list, zeros
 // behind the last.  best, best_g: as scan_row left them; nan: the thread met a
 // NaN.
-template <typename T>
+template <int AT, typename T>
 __device__ __forceinline__ void cta_top(const Row<T>& row, int lo, int hi, int top, float best, int best_g,
-                                        bool nan, TopShared& sh) {
+                                        bool nan, TopShared<AT>& sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // a thread that met nothing above -inf stands for its first vector, if it
   // has one; where that may hold NaN only, with the lowest key there is
   const int own_g = best_g >= 0 ? best_g : lo + tid;
   const uint64_t mine = own_g >= hi ? 0ull : (best_g < 0 && nan) ? 1ull : full_key(best, (uint32_t)own_g);
   uint64_t q = mine;
-  q = max(q, __shfl_xor_sync(0xffffffffu, q, 1));
-  q = max(q, __shfl_xor_sync(0xffffffffu, q, 2));
-  if ((lane & 3) == 0) sh.sets[tid >> 2] = q;
+#pragma unroll
+  for (int o = 1; o < AT / TOP_SETS; o *= 2) q = max(q, __shfl_xor_sync(0xffffffffu, q, o));
+  if (tid % (AT / TOP_SETS) == 0) sh.sets[tid / (AT / TOP_SETS)] = q;
   if (tid == 0) {
     sh.n_flagged = 0;
     sh.n_cand = 0;
@@ -342,6 +362,7 @@ __device__ __forceinline__ void cta_top(const Row<T>& row, int lo, int hi, int t
   if (tid < TOP_SETS) {
     const uint64_t key = sh.sets[tid];
     int rank = 0;
+#pragma unroll 16
     for (int i = 0; i < TOP_SETS; ++i) {
       const uint64_t o = sh.sets[i];
       rank += (o > key || (o == key && i < tid)) ? 1 : 0;
@@ -355,25 +376,38 @@ __device__ __forceinline__ void cta_top(const Row<T>& row, int lo, int hi, int t
   if (mine != 0 && mine >= bound) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = tid;
   __syncthreads();
   const int per = (hi - lo + AT - 1) / AT, items = sh.n_flagged * per;
-  for (int i = tid; i < items; i += AT) {
-    const int g = lo + sh.flagged[i / per] + (i % per) * AT;
-    if (g >= hi) continue;
-    float x[8];
-    decode<T>(row.load(g), x);
-    const int c = row.col(g);
+  const float floor_x = bound > 1 ? key_value((uint32_t)(bound >> 32)) : -INFINITY;
+  constexpr int RU = 4;  // loads in flight
+  for (int i0 = tid; i0 < items; i0 += AT * RU) {
+    Raw8<T> raw[RU];
+    int gs[RU];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (c + j < 0 || c + j >= row.v || x[j] != x[j]) continue;
-      if (full_key(x[j], (uint32_t)g) >= bound) {
-        const int at = atomicAdd(&sh.n_cand, 1);
-        if (at < CAND) sh.cand[at] = full_key(x[j], (uint32_t)(c + j));
+    for (int u = 0; u < RU; ++u) {
+      const int i = i0 + u * AT;
+      gs[u] = i < items ? lo + sh.flagged[i / per] + (i % per) * AT : hi;
+      if (gs[u] < hi) raw[u] = row.load(gs[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      if (gs[u] >= hi) continue;
+      float x[8];
+      decode<T>(raw[u], x);
+      const float mx = fmax3(fmax3(fmax3(x[0], x[1], x[2]), x[3], x[4]), fmaxf(x[5], x[6]), x[7]);
+      if (!(mx >= floor_x)) continue;  // few vectors hold a candidate
+      const int c = row.col(gs[u]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (x[j] >= floor_x && c + j >= 0 && c + j < row.v && full_key(x[j], (uint32_t)gs[u]) >= bound) {
+          const int at = atomicAdd(&sh.n_cand, 1);
+          if (at < CAND) sh.cand[at] = full_key(x[j], (uint32_t)(c + j));
+        }
       }
     }
   }
   __syncthreads();
   const int n = sh.n_cand;
   if (n <= CAND) {
-    rank_keys(sh.cand, n, top, [&](int at, uint64_t key) { sh.list[at] = key; });
+    rank_keys<AT>(sh.cand, n, top, [&](int at, uint64_t key) { sh.list[at] = key; });
     __syncthreads();
     return;
   }
@@ -419,10 +453,10 @@ struct LogprobArgs {
   int64_t* top_id;
 };
 
-template <typename T, bool TOP, bool CL>
-__global__ void __launch_bounds__(AT, 2) k_token_logprobs(const __grid_constant__ LogprobArgs a) {
-  __shared__ AnsShared sh;
-  __shared__ typename std::conditional<TOP, TopShared, int>::type top_sh;
+template <int AT, typename T, bool TOP, bool CL>
+__global__ void __launch_bounds__(AT, 1024 / AT) k_token_logprobs(const __grid_constant__ LogprobArgs a) {
+  __shared__ AnsShared<AT> sh;
+  __shared__ typename std::conditional<TOP, TopShared<AT>, int>::type top_sh;
   const int rank = CL ? (int)tcx::cluster_ctarank() : 0;
   const int64_t r = CL ? blockIdx.x / (unsigned)a.C : blockIdx.x;
   const Row<T> row(static_cast<const T*>(a.logits) + r * a.ldl, a.v);
@@ -430,9 +464,9 @@ __global__ void __launch_bounds__(AT, 2) k_token_logprobs(const __grid_constant_
   const int hi = CL ? (int)((int64_t)row.nvec * (rank + 1) / a.C) : row.nvec;
   float best;
   int best_g;
-  const Soft part = scan_row<T, true, TOP>(row, lo, hi, LOG2E, best, best_g);
-  if constexpr (TOP) cta_top<T>(row, lo, hi, a.top, best, best_g, part.s != part.s, top_sh);
-  const RowStat st = join_row<T, true, CL>(row, lo, hi, part, a.C, sh);  // (its barriers publish the top lists)
+  const Soft part = scan_row<AT, T, true, TOP>(row, lo, hi, LOG2E, best, best_g);
+  if constexpr (TOP) cta_top<AT, T>(row, lo, hi, a.top, best, best_g, part.s != part.s, top_sh);
+  const RowStat st = join_row<AT, T, true, CL>(row, lo, hi, part, a.C, sh);  // (its barriers publish the top lists)
   if (rank == 0 && threadIdx.x == 0) {
     if (a.logprob) {
       const int64_t t = a.tokens[r];
@@ -456,7 +490,7 @@ __global__ void __launch_bounds__(AT, 2) k_token_logprobs(const __grid_constant_
         for (int i = threadIdx.x; i < n; i += AT)
           top_sh.cand[i] = ld_cluster64(&top_sh.list[i % a.top], i / a.top);
         __syncthreads();
-        rank_keys(top_sh.cand, n, a.top, put);
+        rank_keys<AT>(top_sh.cand, n, a.top, put);
       }
     }
   }
@@ -525,9 +559,9 @@ __device__ __forceinline__ void teacher_row(const DistillArgs& a, int64_t r, Tea
   }
 }
 
-template <typename T, bool CL>
-__global__ void __launch_bounds__(AT, 2) k_topk_distill(const __grid_constant__ DistillArgs a) {
-  __shared__ AnsShared sh;
+template <int AT, typename T, bool CL>
+__global__ void __launch_bounds__(AT, 1024 / AT) k_topk_distill(const __grid_constant__ DistillArgs a) {
+  __shared__ AnsShared<AT> sh;
   __shared__ TeacherShared te;
   const int rank = CL ? (int)tcx::cluster_ctarank() : 0;
   const int64_t r = CL ? blockIdx.x / (unsigned)a.C : blockIdx.x;
@@ -537,8 +571,8 @@ __global__ void __launch_bounds__(AT, 2) k_topk_distill(const __grid_constant__ 
   if (threadIdx.x < 32) teacher_row(a, r, te);
   float best;
   int best_g;
-  const Soft part = scan_row<T, false, false>(row, lo, hi, a.k, best, best_g);
-  const RowStat st = join_row<T, false, CL>(row, lo, hi, part, a.C, sh);
+  const Soft part = scan_row<AT, T, false, false>(row, lo, hi, a.k, best, best_g);
+  const RowStat st = join_row<AT, T, false, CL>(row, lo, hi, part, a.C, sh);
   if (rank == 0 && threadIdx.x < 32) {
     float l = 0.0f;
     for (int e = threadIdx.x; e < a.top; e += 32) {
@@ -554,28 +588,56 @@ __global__ void __launch_bounds__(AT, 2) k_topk_distill(const __grid_constant__ 
     const float w = a.weight ? a.weight[r] : 1.0f;
     const bool zero = w == 0.0f || (!te.live && !te.bad);
     const float c = te.bad ? NAN : w * a.inv_t, cs = st.empty ? c : c / st.a.s;
-    const bool same = ((uintptr_t)(out + row.first) & 15) == 0;  // the output's vectors are aligned too
+    // vectors by the output's alignment now: wide stores, and loads that are
+    // shifted where the two rows are aligned differently
+    const Row<T> dst(out, a.v);
+    const bool same = dst.first == row.first;
+    const int lo2 = CL ? (int)((int64_t)dst.nvec * rank / a.C) : 0;
+    const int hi2 = CL ? (int)((int64_t)dst.nvec * (rank + 1) / a.C) : dst.nvec;
+    const auto fetch = [&](int g) {
+      if (same) return row.load(g);
+      const int col = dst.col(g);
+      if constexpr (sizeof(T) == 2) {
+        if (col >= 0) return load_row8<T>(row.p, col, a.v);
+      }
+      T e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = col + i >= 0 && col + i < a.v ? row.p[col + i] : from_f<T>(0.0f);
+      Raw8<T> r;
+      memcpy(&r, e, sizeof(r));
+      return r;
+    };
     auto prob = [&](float x) {  // p times its row's sum
       if (st.flat) return (!st.empty && x == st.raw) ? 1.0f : 0.0f;
       return ex2(fmaf(x, a.k, -st.a.m));
     };
     constexpr int U = sizeof(T) == 4 ? 2 : 4;
-    for (int g0 = lo + (int)threadIdx.x; g0 < hi; g0 += AT * U) {
+    const uint64_t k2 = f2_pack(a.k, a.k), m2 = f2_pack(-st.a.m, -st.a.m), c2 = f2_pack(cs, cs);
+    for (int g0 = lo2 + (int)threadIdx.x; g0 < hi2; g0 += AT * U) {
       Raw8<T> raw[U];
 #pragma unroll
       for (int j = 0; j < U; ++j)
-        if (g0 + j * AT < hi) raw[j] = row.load(g0 + j * AT);
+        if (g0 + j * AT < hi2) raw[j] = fetch(g0 + j * AT);
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         const int g = g0 + j * AT;
-        if (g >= hi) break;
+        if (g >= hi2) break;
         float x[8];
         decode<T>(raw[j], x);
+        if (st.flat || zero) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = zero ? 0.0f : cs * prob(x[i]);
-        const int col = row.col(g);
+          for (int i = 0; i < 8; ++i) x[i] = zero ? 0.0f : cs * prob(x[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y0, y1;
+            f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), k2, m2), y0, y1);
+            f2_unpack(f2_mul(f2_pack(ex2(y0), ex2(y1)), c2), x[2 * i], x[2 * i + 1]);
+          }
+        }
+        const int col = dst.col(g);
         if (col >= 0 && col + 8 <= a.v) {
-          store_vec<8>(out + col, x, same);
+          store_vec<8>(out + col, x, true);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -586,7 +648,7 @@ __global__ void __launch_bounds__(AT, 2) k_topk_distill(const __grid_constant__ 
     // the teacher's entries in this CTA's columns, each from p and q at once
     // (one rounding); the first of equal ids takes them all
     __syncthreads();
-    const int c_lo = row.col(lo), c_hi = row.col(hi);
+    const int c_lo = dst.col(lo2), c_hi = dst.col(hi2);
     for (int e = threadIdx.x; e < a.top && !zero; e += AT) {
       const int id = te.id[e];
       if (id < c_lo || id >= c_hi || id < 0) continue;
@@ -614,10 +676,11 @@ int row_ctas(int64_t rows, int64_t v, int sms) {
 }
 
 template <typename A>
-mpq_status launch_rows(void (*one)(A), void (*many)(A), const A& a, int C, cudaStream_t st, const char* name) {
+mpq_status launch_rows(void (*one)(A), void (*many)(A), const A& a, int threads, cudaStream_t st, const char* name) {
+  const int C = a.C;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * C));
-  cfg.blockDim = dim3(AT);
+  cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -632,14 +695,30 @@ mpq_status launch_rows(void (*one)(A), void (*many)(A), const A& a, int C, cudaS
   return check_launch(name);
 }
 
+// Whether four CTAs an SM, a row each, would hold more than L2 does: then two of
+// twice the threads.
+template <typename T>
+bool large_rows(int C, int64_t v) {
+  return C == 1 && 4ll * 148 * v * (int64_t)sizeof(T) > L2_ROWS;
+}
+
 template <typename T>
 mpq_status run_logprobs(const LogprobArgs& a, cudaStream_t st) {
-  if (a.top) return launch_rows(k_token_logprobs<T, true, false>, k_token_logprobs<T, true, true>, a, a.C, st, "k_token_logprobs");
-  return launch_rows(k_token_logprobs<T, false, false>, k_token_logprobs<T, false, true>, a, a.C, st, "k_token_logprobs");
+  // (the columns that are read again should still be in L2: 1024 rows of
+  // 131072 bf16 with 64 alternatives take 92 us with 512 threads, 104 with 256;
+  // 4096 rows of 32000 with 20 take 125 and 101)
+  if (a.top && large_rows<T>(a.C, a.v))
+    return launch_rows(k_token_logprobs<512, T, true, false>, k_token_logprobs<512, T, true, true>, a, 512, st, "k_token_logprobs");
+  if (a.top) return launch_rows(k_token_logprobs<256, T, true, false>, k_token_logprobs<256, T, true, true>, a, 256, st, "k_token_logprobs");
+  return launch_rows(k_token_logprobs<256, T, false, false>, k_token_logprobs<256, T, false, true>, a, 256, st, "k_token_logprobs");
 }
 template <typename T>
 mpq_status run_distill(const DistillArgs& a, cudaStream_t st) {
-  return launch_rows(k_topk_distill<T, false>, k_topk_distill<T, true>, a, a.C, st, "k_topk_distill");
+  // the second reading of a row should find it in L2 (1024 rows of 131072
+  // bf16: 132 us with 512 threads, 145 with 256; 4096 rows of 32000: 139, 122)
+  const bool large = a.dlogits && large_rows<T>(a.C, a.v);
+  if (large) return launch_rows(k_topk_distill<512, T, false>, k_topk_distill<512, T, true>, a, 512, st, "k_topk_distill");
+  return launch_rows(k_topk_distill<256, T, false>, k_topk_distill<256, T, true>, a, 256, st, "k_topk_distill");
 }
 
 mpq_status rows_check(const char* who, int64_t rows, int64_t v, int32_t dtype) {

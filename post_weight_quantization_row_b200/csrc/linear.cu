@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(256)
 // sums the unrounded values), and per block of 64 rows the column sums.
 constexpr int DZ_ROWS = 64;
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
     k_lin_dz(const T* __restrict__ dy, int64_t ldy, const T* __restrict__ z, int64_t ldz, int act,
              int64_t rows, int64_t n, T* __restrict__ dz, int64_t ldd, float* __restrict__ part,
              bool vec_y, bool vec_z) {
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(256)
   F8 sum = {};
   if (c < n) {
     const int left = (int)min((int64_t)8, n - c);
-    constexpr int NR = 4;  // rows in flight
+    constexpr int NR = 2;  // rows in flight
     for (int64_t r0 = r_lo + rl; r0 < r_hi; r0 += 8 * NR) {
       Raw8<T> gy[NR], zz[NR];
 #pragma unroll

@@ -154,7 +154,9 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     z = x.new_empty(shape) if preact else None
     if rows > 0:
         px, pw = x.data_ptr(), weight.data_ptr()
-        nbytes = lib.mpq_linear_workspace_bytes(px, ldx, pw, ldw, rows, n, k)
+        nbytes = 0  # (as the library says where nothing is unaligned, without asking it)
+        if (px | pw) & 15 or (ldx | ldw) & 7 or ldx < k or ldw < k:
+            nbytes = lib.mpq_linear_workspace_bytes(px, ldx, pw, ldw, rows, n, k)
         keep, ws = _scratch(nbytes, x)
         _call(lib.mpq_linear, "mpq_linear", x.device, px, ldx, pw, ldw, rows, n, k, DTYPES[x.dtype], pb,
               DTYPES[bias.dtype] if bias is not None else 0, act, pr, ldr,

@@ -1,8 +1,8 @@
 """token_logprobs and topk_distill against plain 64-bit formulas, and the run
 of all layer operators around a solve.
 
-Tolerances: a softmax sum over v logits is added by 512 threads, v / 512
-sequential fp32 adds each and a tree, exponentials good to 2^-22 and scaled
+Tolerances: a softmax sum over v logits is added by 256 threads or more, in two
+chains each: v / 512 sequential fp32 adds and a tree, exponentials good to 2^-22 and scaled
 logits rounded by 2^-24 of their size; `rel(v)` is the sum of these."""
 import math
 
@@ -122,7 +122,7 @@ def test_logprobs_of_slices_and_masks(mpq, dtype):
 
 
 def test_logprobs_with_most_of_the_large_logits_in_few_threads(mpq):
-    # columns 8 g + 0..7 with g = 3 mod 512 belong to one thread: its columns
+    # columns 8 g + 0..7 with g = 3 mod 256 belong to one thread: its columns
     # alone hold more large logits than the candidate buffer
     v = 512 * 8 * 40
     for rows in (1, 300):
