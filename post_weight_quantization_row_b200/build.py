@@ -1,6 +1,7 @@
 """Build libmpq.so in-tree for sm_100a with nvcc (object files under _build/)."""
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -26,7 +27,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     hdr_time = max((os.path.getmtime(h) for h in _headers()), default=0.0)
-    objs = []
+    objs, cmds = [], []
     for src in sources:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -36,7 +37,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
             cmd = [NVCC, *ARCH, *FLAGS, "-c", src, "-o", obj]
             if verbose:
                 print(" ".join(cmd), flush=True)
-            subprocess.run(cmd, check=True)
+            cmds.append(cmd)
+    with concurrent.futures.ThreadPoolExecutor(max(1, os.cpu_count() or 1)) as pool:
+        for done in [pool.submit(subprocess.run, cmd, check=True) for cmd in cmds]:
+            done.result()
     lib_stale = force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(
         os.path.getmtime(o) for o in objs)
     if lib_stale:

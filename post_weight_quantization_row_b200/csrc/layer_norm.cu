@@ -71,14 +71,15 @@ struct LnArgs {
   int G, C;
 };
 
-// How the parameters come: none, both in T, both in fp32 (rows and parameters
-// then start on 16-byte boundaries and hold whole vectors of 8), or ANY: the
-// general form, element by element.
-enum { PM_NONE = 0, PM_T = 1, PM_F32 = 2, PM_ANY = 3 };
+// How rows and parameters come.  Parameters: none, all in T, all in fp32, on
+// 16-byte boundaries.  Rows: on 16-byte boundaries and of whole vectors of 8,
+// or PM_SHIFT: at any address and of any length (from 129 on, so that a warp
+// holds one row).  PM_ANY: everything else, element by element.
+enum { PM_NONE = 0, PM_T = 1, PM_F32 = 2, PM_ANY = 3, PM_SHIFT = 4 };
 
-// The column of element i of vector j of a thread t of G: 8 neighbours, one
-// or two wide accesses, or for PM_ANY single elements G apart, so that a
-// warp's accesses still cover neighbouring ones.
+// The column of element i of vector j of a thread t of G: 8 neighbours, or for
+// PM_ANY single elements G apart, so that a warp's accesses still cover
+// neighbouring ones.
 template <int PM>
 __device__ __forceinline__ int ln_col(int t, int G, int j, int i) {
   return PM != PM_ANY ? (t + j * G) * 8 + i : (j * 8 + i) * G + t;
@@ -88,6 +89,12 @@ __device__ __forceinline__ Raw8<T> ln_load(const T* row, int n, int t, int G, in
   Raw8<T> r;
   if (PM != PM_ANY) {
     const int c = (t + j * G) * 8;
+    if (PM & PM_SHIFT) {
+      if (c < n) return load_row8<T>(row, c, n);
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.q[i] = make_uint4(0, 0, 0, 0);
+      return r;
+    }
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
       r.q[i] = c < n ? reinterpret_cast<const uint4*>(row + c)[i] : make_uint4(0, 0, 0, 0);
@@ -99,11 +106,22 @@ __device__ __forceinline__ Raw8<T> ln_load(const T* row, int n, int t, int G, in
   memcpy(&r, e, sizeof(r));
   return r;
 }
+// A warp's staging for rows at any address
 template <int PM, typename T>
-__device__ __forceinline__ void ln_store(T* row, const float (&v)[8], int n, int t, int G, int j) {
+struct Stage {
+  uint4 v[PM != PM_ANY && (PM & PM_SHIFT) ? 32 * (16 * sizeof(T) + 1) : 1];
+  __device__ __forceinline__ T* warp() { return reinterpret_cast<T*>(v + (threadIdx.x >> 5) * (16 * sizeof(T) + 1)); }
+};
+template <int PM, typename T>
+__device__ __forceinline__ void ln_store(T* row, const float (&v)[8], int n, int t, int G, int j, Stage<PM, T>& stage) {
   if (PM != PM_ANY) {
     const int c = (t + j * G) * 8;
-    if (c < n) store_vec<8>(row + c, v, true);
+    if (PM & PM_SHIFT) {
+      const int cw = c - (int)(threadIdx.x & 31) * 8;  // the warp's first column
+      if (cw < n) warp_store<T>(row + cw, v, min(256, n - cw), stage.warp());
+    } else if (c < n) {
+      store_vec<8>(row + c, v, true);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -115,12 +133,13 @@ __device__ __forceinline__ void ln_param(const LnArgs& a, const void* p, float d
   const int n = (int)a.n;
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = dflt;
-  if (PM == PM_NONE) return;
+  if ((PM & 3) == PM_NONE) return;
   if (PM != PM_ANY) {
     const int c = (t + j * a.G) * 8;
     if (c >= n) return;
-    if (PM == PM_T) load_vec<8>(static_cast<const T*>(p) + c, w, true);
-    else load_vec<8>(static_cast<const float*>(p) + c, w, true);
+    const int have = (PM & PM_SHIFT) ? n - c : 8;
+    if ((PM & 3) == PM_T) load_edge<8>(static_cast<const T*>(p) + c, w, have, true);
+    else load_edge<8>(static_cast<const float*>(p) + c, w, have, true);
     return;
   }
   if (!p) return;
@@ -143,6 +162,7 @@ __global__ void __launch_bounds__(NV * NR >= 8 ? 256 : 1024)
     k_ln_fwd(const __grid_constant__ LnArgs a, float eps, T* __restrict__ y, float* __restrict__ mean_out,
              float* __restrict__ rstd_out) {
   __shared__ __align__(16) float scratch[2 * 32 * NR];
+  __shared__ Stage<PM, T> stage;
   int buf = 0;
   const int t = threadIdx.x & (a.G - 1);
   const int64_t row0 = ((int64_t)blockIdx.x * (blockDim.x / a.G) + threadIdx.x / a.G) * NR;
@@ -183,7 +203,8 @@ __global__ void __launch_bounds__(NV * NR >= 8 ? 256 : 1024)
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[r][j].p[i] = f2_add(v[r][j].p[i], m2);
-      if (PM == PM_ANY) {  // columns that do not exist hold -mean: out
+      // columns that do not exist hold -mean: out
+      if (PM == PM_ANY || ((PM & PM_SHIFT) && (t + j * a.G) * 8 + 8 > n)) {
         float e[8];
         unpairs(v[r][j], e);
 #pragma unroll
@@ -223,7 +244,7 @@ __global__ void __launch_bounds__(NV * NR >= 8 ? 256 : 1024)
       for (int i = 0; i < 4; ++i) v[r][j].p[i] = f2_fma(f2_mul(v[r][j].p[i], r2), w2.p[i], b2.p[i]);
       float o[8];
       unpairs(v[r][j], o);
-      ln_store<PM, T>(y + (row0 + r) * a.n, o, n, t, a.G, j);
+      ln_store<PM, T>(y + (row0 + r) * a.n, o, n, t, a.G, j, stage);
     }
   }
 }
@@ -287,6 +308,7 @@ __global__ void __launch_bounds__(NV == 1 ? 128 : 512)
              const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
              float* __restrict__ part) {
   __shared__ __align__(16) float scratch[2 * 64];
+  __shared__ Stage<PM, T> stage;
   __shared__ float meet[2][2];     // CL: this CTA's sums, alternating between rows
   extern __shared__ float join[];  // several groups: dw[n], db[n]
   int buf = 0;
@@ -374,7 +396,7 @@ __global__ void __launch_bounds__(NV == 1 ? 128 : 512)
           for (int i = 0; i < 4; ++i)
             g[j].p[i] = f2_mul(q2, f2_fma(xh[j].p[i], s1, f2_add(g[j].p[i], s0)));
           unpairs(g[j], o);
-          ln_store<PM, T>(dx + row * a.n + c0, o, n, t, a.G, j);
+          ln_store<PM, T>(dx + row * a.n + c0, o, n, t, a.G, j, stage);
         }
       }
     }
@@ -395,7 +417,7 @@ __global__ void __launch_bounds__(NV == 1 ? 128 : 512)
   if (groups == 1) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (PM != PM_ANY) {
+      if (PM != PM_ANY && !(PM & PM_SHIFT)) {
         const int c = (t + j * a.G) * 8;
         if (c < n) {
           store_vec<8>(pw + c, dw[j], true);
@@ -579,7 +601,13 @@ mpq_status ln_fwd(const LnArgs& a, double eps, void* y, float* mean, float* rstd
   const float e = (float)eps;
   ProfScope ps_("k_layer_norm", st);
   if (a.n > LN_REG_MAX) k_ln_fwd_wide<T><<<(unsigned)a.rows, 1024, 0, st>>>(a, e, yo, mean, rstd);
-  else if (!a.x_vec || !a.p_vec || !a.o_vec || a.n % 8 || !a.w != !a.b) ln_fwd_rows<T, PM_ANY>(a, e, yo, mean, rstd, st);
+  else if (!a.p_vec || !a.w != !a.b) ln_fwd_rows<T, PM_ANY>(a, e, yo, mean, rstd, st);
+  else if (!a.x_vec || !a.o_vec || a.n % 8) {
+    if (a.n <= 128) ln_fwd_rows<T, PM_ANY>(a, e, yo, mean, rstd, st);
+    else if (!a.w) ln_fwd_rows<T, PM_NONE | PM_SHIFT>(a, e, yo, mean, rstd, st);
+    else if (a.p_f32) ln_fwd_rows<T, PM_F32 | PM_SHIFT>(a, e, yo, mean, rstd, st);
+    else ln_fwd_rows<T, PM_T | PM_SHIFT>(a, e, yo, mean, rstd, st);
+  }
   else if (!a.w) ln_fwd_rows<T, PM_NONE>(a, e, yo, mean, rstd, st);
   else if (a.p_f32) ln_fwd_rows<T, PM_F32>(a, e, yo, mean, rstd, st);
   else ln_fwd_rows<T, PM_T>(a, e, yo, mean, rstd, st);
@@ -644,7 +672,11 @@ mpq_status ln_bwd(LnArgs a, const void* dy, int64_t ldy, bool y_vec, const float
       return sums ? ln_bwd_rows<T, PM, true>(a, dyp, ldy, mean, rstd, dxp, part, &blocks, st)
                   : ln_bwd_rows<T, PM, false>(a, dyp, ldy, mean, rstd, dxp, part, &blocks, st);
     };
-    if (!a.x_vec || !y_vec || !a.p_vec || !a.o_vec || a.n % 8) MPQ_TRY(go(std::integral_constant<int, PM_ANY>{}));
+    const bool rows_vec = a.x_vec && y_vec && a.o_vec && a.n % 8 == 0;
+    if (!a.p_vec || (!rows_vec && a.n <= 128)) MPQ_TRY(go(std::integral_constant<int, PM_ANY>{}));
+    else if (!rows_vec && !a.w) MPQ_TRY(go(std::integral_constant<int, PM_NONE | PM_SHIFT>{}));
+    else if (!rows_vec && a.p_f32) MPQ_TRY(go(std::integral_constant<int, PM_F32 | PM_SHIFT>{}));
+    else if (!rows_vec) MPQ_TRY(go(std::integral_constant<int, PM_T | PM_SHIFT>{}));
     else if (!a.w) MPQ_TRY(go(std::integral_constant<int, PM_NONE>{}));
     else if (a.p_f32) MPQ_TRY(go(std::integral_constant<int, PM_F32>{}));
     else MPQ_TRY(go(std::integral_constant<int, PM_T>{}));

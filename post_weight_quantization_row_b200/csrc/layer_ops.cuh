@@ -193,33 +193,66 @@ __device__ __forceinline__ Raw8<T> load_raw(const T* p, int n, bool vec) {
   return r;
 }
 
-// Elements at .. at + 7 of a row of n 16-bit elements at any address, those
-// past the end 0.  Two aligned 16-byte loads and a shift where both lie within
-// the row, single elements at its ends.
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_row8(const T* row, int at, int n) {
-  static_assert(sizeof(T) == 2, "16-bit elements");
-  const T* p = row + at;
-  const uintptr_t a = (uintptr_t)p;
-  if ((a & 15) == 0) return load_raw<T>(p, n - at, true);
-  const int off = (int)(a & 15) >> 1;  // elements past the boundary
-  if (at < off || at - off + 16 > n) return load_raw<T>(p, n - at, false);
-  const uint4* q = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
-  const uint4 u = q[0], v = q[1];
+// Words s .. s + 3 of 8, counted in bytes 2 s2 .. (0 .. 14): a 16-byte window at
+// any even byte of two vectors.
+__device__ __forceinline__ uint4 window16(const uint4& u, const uint4& v, int halfwords) {
   uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-  if (off & 4) {
+  if (halfwords & 4) {
 #pragma unroll
     for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
   }
-  if (off & 2) {
+  if (halfwords & 2) {
 #pragma unroll
     for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
   }
-  const uint32_t s = (off & 1) * 16;
+  const uint32_t s = (halfwords & 1) * 16;
+  return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                    __funnelshift_r(w[3], w[4], s));
+}
+// Elements at .. at + 7 of a row of n elements at any address, those past the
+// end 0.  Aligned 16-byte loads and shifts where all of them lie within the
+// row, single elements at its ends.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_row8(const T* row, int at, int n) {
+  const T* p = row + at;
+  const uintptr_t a = (uintptr_t)p;
+  if ((a & 15) == 0) return load_raw<T>(p, n - at, true);
+  constexpr int V = 16 / (int)sizeof(T);  // elements of a 16-byte vector
+  const int off = (int)(a & 15) / (int)sizeof(T);  // elements past the boundary
+  if (at < off || at - off + 8 + V > n) return load_raw<T>(p, n - at, false);
+  const uint4* q = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
   Raw8<T> r;
-  r.q[0] = make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
-                      __funnelshift_r(w[3], w[4], s));
+  uint4 u = q[0];
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) {
+    const uint4 v = q[i + 1];
+    r.q[i] = window16(u, v, (int)(a & 15) >> 1);
+    u = v;
+  }
   return r;
+}
+// Stores a warp's 8 elements a lane, 256 neighbours of a row of which `total`
+// exist, at any address: through `stage` (shared memory of the warp, 256
+// elements and 16 bytes, on a 16-byte boundary) to whole aligned vectors, and
+// single elements at the ends.  All lanes take part.
+template <typename T>
+__device__ __forceinline__ void warp_store(T* row, const float (&v)[8], int total, T* stage) {
+  const int lane = threadIdx.x & 31;
+  constexpr int V = 16 / (int)sizeof(T);
+  __syncwarp();
+  store_vec<8>(stage + lane * 8, v, true);
+  __syncwarp();
+  const int past = (int)((uintptr_t)row & 15) / (int)sizeof(T), lead = min(total, past ? V - past : 0);
+  const int nv = (total - lead) / V;
+  const uint4* q = reinterpret_cast<const uint4*>(stage);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) {
+    const int k = lane + 32 * i;
+    if (k < nv)
+      reinterpret_cast<uint4*>(row + lead)[k] = lead ? window16(q[k], q[k + 1], lead * (int)sizeof(T) / 2) : q[k];
+  }
+  const int e = lane < lead ? lane : lead + nv * V + (lane - lead);
+  if (e < total) row[e] = stage[e];
 }
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 ulp; 0 below 2^-126

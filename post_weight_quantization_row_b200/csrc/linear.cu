@@ -18,6 +18,13 @@
 // with a warp per row of it (and any alignment).
 // The epilogue adds the bias, applies the activation, adds the residual and
 // rounds once, in fp32 before that.
+//
+// The tensor cores' accumulator drops what falls below its last bit instead of
+// rounding it, so a long chain of products drifts towards zero: 2.4e-6 of the
+// result over a contraction of 2000, 8.7e-6 over 14336.  Results of 16 bits
+// hide that (their own half step is 5e-4 or 4e-3); for fp32 results a chain
+// ends after CHAIN steps and the chains are added, rounded, in the epilogue's
+// registers, which keeps the error below 1e-6 at any length.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -183,6 +190,7 @@ __device__ __forceinline__ void act_grad8(F8& g, const F8& z, int act) {
 // ------------------------------------------------------------- the operand --
 constexpr int BK = 64;              // contraction per stage
 constexpr int BOX = 64 * 64 * 2;    // bytes of a 64 x 64 box (8 KiB)
+constexpr int CHAIN = 8;            // steps accumulated at a stretch for fp32 results
 
 // Operand tiles of 64 (contraction) x 64 .. 128, with 128-byte swizzle.
 // K-major (rows of 64 contraction elements): 8 rows are 1024 B apart; 16
@@ -311,12 +319,13 @@ static_assert(P_SMEM <= 232448, "pair kernel's shared memory");
 struct Walk {
   int mt, nt, whole, total;
 };
-__host__ __device__ inline Walk make_walk(int rows, int cols, int workers) {
+// (halves: 128-column tiles only, whose sums fit the epilogue's registers.)
+__host__ __device__ inline Walk make_walk(int rows, int cols, int workers, bool halves) {
   Walk w;
   w.mt = (rows + PT - 1) / PT;
   w.nt = (cols + PT - 1) / PT;
   const int t = w.mt * w.nt, left = t % workers;
-  w.whole = 2 * left <= workers ? t - left : t;
+  w.whole = halves ? 0 : 2 * left <= workers ? t - left : t;
   w.total = w.whole + 2 * (t - w.whole);
   return w;
 }
@@ -357,7 +366,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // rank 0 issues the pair's MMAs
   const int worker = (int)cluster_id_x(), nworkers = (int)(gridDim.x / 2);
-  const Walk walk = make_walk(o.rows, o.cols, nworkers);
+  constexpr bool CHAINS = std::is_same<O, float>::value;
+  const Walk walk = make_walk(o.rows, o.cols, nworkers, CHAINS);
   const int KT = (KC + BK - 1) / BK;
   const int stages = walk.whole ? 6 : 8, stage = walk.whole ? P_RING / 6 : P_RING / 8;
 
@@ -434,43 +444,42 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t ID_W = lin_idesc<T, A_MN, B_MN>(256, PT), ID_N = lin_idesc<T, A_MN, B_MN>(256, PT / 2);
     const uint64_t da0 = op_desc<A_MN>(smem_u32(smem)), db0 = op_desc<B_MN>(smem_u32(smem) + 128 * BK * 2);
-    uint32_t tl = 0;
+    const int CH = CHAINS ? CHAIN : KT;
+    uint32_t tl = 0;  // accumulators filled
     int s = 0;
     uint32_t phase = 0;
     bool ok = true, ready = false;
-    for (int t = worker; t < walk.total && ok; t += nworkers, ++tl) {
-      const int buf = tl & 1;
+    for (int t = worker; t < walk.total; t += nworkers) {
       const uint32_t idesc = t < walk.whole ? ID_W : ID_N;
-      if (tl >= 2 && !mbar_wait_cl(&tm_empty[buf], (tl / 2 - 1) & 1)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)buf * PT;
-      for (int kt = 0; kt < KT; ++kt) {
-        if (!ready && !mbar_wait_cl(&full[s], phase)) {
-          ok = false;
-          break;
-        }
+      for (int k0 = 0; k0 < KT; k0 += CH, ++tl) {  // a chain into an accumulator
+        const int buf = tl & 1, n = min(CH, KT - k0);
+        // elect.sync needs every lane, so a wait that runs out ends no loop: its
+        // lane waits no more, and the result is reported as undefined
+        if (ok && tl >= 2) ok = mbar_wait_cl(&tm_empty[buf], (tl / 2 - 1) & 1);
         tc_fence_after();
-        const uint64_t da = da0 + (uint32_t)s * (uint32_t)(stage >> 4), db = db0 + (uint32_t)s * (uint32_t)(stage >> 4);
-        uint64_t* freed = &empty[s];
-        if (++s == stages) {
-          s = 0;
-          phase ^= 1;
-        }
-        ready = mbar_done_cl(&full[s], phase);
-        if (elect_one()) {
+        const uint32_t d = tmem + (uint32_t)buf * PT;
+        for (int kt = 0; kt < n; ++kt) {
+          if (ok && !ready) ok = mbar_wait_cl(&full[s], phase);
+          tc_fence_after();
+          const uint64_t da = da0 + (uint32_t)s * (uint32_t)(stage >> 4), db = db0 + (uint32_t)s * (uint32_t)(stage >> 4);
+          uint64_t* freed = &empty[s];
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+          }
+          ready = mbar_done_cl(&full[s], phase);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            umma_f16_cg2(d, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (kt | kk) != 0 ? 1u : 0u);
-          commit_both(freed);
-          if (kt == KT - 1) commit_both(&tm_full[buf]);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              umma_f16_cg2(d, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (kt | kk) != 0 ? 1u : 0u);
+            commit_both(freed);
+            if (kt == n - 1) commit_both(&tm_full[buf]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
-    if (!ok && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    if (!ok) atomicOr(&g_lin_status, STATUS_TIMEOUT);
     for (uint32_t q = (tl > 2 ? tl - 2 : 0); q < tl; ++q)  // MMAs finish before TMEM is freed
       for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&tm_full[q & 1], (q / 2) & 1); ++i)
         if (i > 256) __nanosleep(64);
@@ -485,7 +494,6 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const bool wide = o.out_vec && (!o.residual || o.res_vec);
     uint32_t tl = 0;
     for (int t = worker; t < walk.total; t += nworkers, ++tl) {
-      const int buf = tl & 1;
       int m0, n0, wn;
       walk_tile(walk, t, m0, n0, wn);
       const int row0 = m0 + (int)rank * 128 + q * 32;
@@ -496,12 +504,37 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(rl + min(c + 31, o.cols - 1)));
         }
       }
-      const bool ok = __all_sync(0xffffffffu, mbar_wait_cl(&tm_full[buf], (tl / 2) & 1));
+      // CHAINS: the chains of this warp's two 32-column chunks, added up
+      float sum0[CHAINS ? 32 : 1], sum1[CHAINS ? 32 : 1];
+      bool ok = true;
+      if constexpr (CHAINS) {
+        for (int k = 0; k < KT && ok; k += CHAIN) {
+          const int buf = tl & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait_cl(&tm_full[buf], (tl / 2) & 1));
+          tc_fence_after();
+          const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * PT + side * 32);
+          uint32_t a[32], b[32];
+          tmem_ld32(tb, a);
+          tmem_ld32(tb + 64, b);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            sum0[i] = (k ? sum0[i] : 0.0f) + __uint_as_float(a[i]);
+            sum1[i] = (k ? sum1[i] : 0.0f) + __uint_as_float(b[i]);
+          }
+          if (k + CHAIN < KT) ++tl;
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait_cl(&tm_full[tl & 1], (tl / 2) & 1));
+        tc_fence_after();
+      }
       if (!ok) {
         if (lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
         break;
       }
-      tc_fence_after();
+      const int buf = tl & 1;
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)buf * PT;
       for (int c0 = side * 32; c0 < wn; c0 += 64) {
         const int left = o.cols - (n0 + c0), top = o.rows - row0;  // columns and rows from this chunk on
@@ -520,13 +553,19 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           }
         }
         uint32_t v[32];
-        tmem_ld32(tbase + (uint32_t)c0, v);
-        if (c0 + 64 >= wn) {  // this warp's part is read: hand the accumulator back
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);
+        if constexpr (CHAINS) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(c0 < 64 ? sum0[i] : sum1[i]);
+        } else {
+          tmem_ld32(tbase + (uint32_t)c0, v);
+          if (c0 + 64 >= wn) {  // this warp's part is read: hand the accumulator back
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);
+          }
         }
         if (left <= 0 || top <= 0) continue;
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           stg[lane * 8 + (k ^ (lane & 7))] =
@@ -617,6 +656,15 @@ struct SplitGeom {
   uint32_t tmem_cols;
 };
 __host__ __device__ inline int split_stage_bytes(int NT) { return 128 * BK * 2 + NT * BK * 2; }
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
 // Elements of a partial tile (row-major, 128 columns) that each of S CTAs
 // joins: whole runs of 32.
 __host__ __device__ inline int split_share(int rows, int S) { return ((rows * 128 + S - 1) / S + 31) / 32 * 32; }
@@ -635,7 +683,10 @@ __global__ void __launch_bounds__(S_THREADS)
   uint64_t* empty = full + g.stages;
   uint64_t* done = empty + g.stages;
   uint64_t* arrived = done + 1;  // S > 1: every CTA's part of this CTA's share is in recv
-  uint32_t* tmem_slot = (uint32_t*)(arrived + 1);
+  uint64_t* ch_full = arrived + 1;  // chains (fp32 results): two accumulators in turn
+  uint64_t* ch_empty = ch_full + 2;
+  uint32_t* tmem_slot = (uint32_t*)(ch_empty + 2);
+  constexpr bool CHAINS = std::is_same<O, float>::value;
 
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = g.S > 1 ? (int)cluster_ctarank() : 0;
@@ -652,6 +703,10 @@ __global__ void __launch_bounds__(S_THREADS)
     }
     mbar_init(done, 1);
     mbar_init(arrived, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ch_full[b], 1);
+      mbar_init(&ch_empty[b], 8);  // the epilogue warps
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (g.S > 1) mbar_expect_tx(arrived, (uint32_t)(g.S * max(e_hi - e_lo, 0) * 4));
@@ -695,35 +750,74 @@ __global__ void __launch_bounds__(S_THREADS)
   } else if (warp == 1) {
     const uint32_t idesc = lin_idesc<T, A_MN, B_MN>(128, g.NT);
     const uint64_t da0 = op_desc<A_MN>(smem_u32(smem)), db0 = op_desc<B_MN>(smem_u32(smem) + 128 * BK * 2);
+    const int CH = CHAINS ? CHAIN : nk;
     int s = 0;
-    uint32_t phase = 0;
-    bool ready = false;
-    for (int i = 0; i < nk; ++i) {
-      if (!ready && !mbar_wait(&full[s], phase)) {
-        if (lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
-        break;
+    uint32_t phase = 0, tl = 0;
+    bool ok = true, ready = false;
+    for (int i0 = 0; i0 < nk; i0 += CH, ++tl) {
+      const int buf = CHAINS ? (int)(tl & 1) : 0, n = min(CH, nk - i0);
+      // (as in the pair kernel, a wait that runs out ends no loop)
+      if (CHAINS) {
+        if (ok && tl >= 2) ok = mbar_wait(&ch_empty[buf], (tl / 2 - 1) & 1);
+        tc_fence_after();
       }
-      tc_fence_after();
-      const uint64_t da = da0 + (uint32_t)s * (uint32_t)(stage >> 4), db = db0 + (uint32_t)s * (uint32_t)(stage >> 4);
-      uint64_t* freed = &empty[s];
-      if (++s == g.stages) {
-        s = 0;
-        phase ^= 1;
-      }
-      ready = mbar_test_wait(&full[s], phase);
-      if (elect_one()) {
+      const uint32_t d = tmem + (uint32_t)buf * (g.tmem_cols / 2);
+      for (int i = 0; i < n; ++i) {
+        if (ok && !ready) ok = mbar_wait(&full[s], phase);
+        tc_fence_after();
+        const uint64_t da = da0 + (uint32_t)s * (uint32_t)(stage >> 4), db = db0 + (uint32_t)s * (uint32_t)(stage >> 4);
+        uint64_t* freed = &empty[s];
+        if (++s == g.stages) {
+          s = 0;
+          phase ^= 1;
+        }
+        ready = mbar_test_wait(&full[s], phase);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          umma_f16(tmem, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (i | kk) != 0 ? 1u : 0u);
-        umma_commit(freed);
+          for (int kk = 0; kk < BK / 16; ++kk)
+            umma_f16(d, da + kk * KSTEP<A_MN>, db + kk * KSTEP<B_MN>, idesc, (i | kk) != 0 ? 1u : 0u);
+          umma_commit(freed);
+          if (CHAINS && i == n - 1) umma_commit(&ch_full[buf]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
+    if (!ok) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    __syncwarp();
     if (elect_one()) umma_commit(done);
     __syncwarp();
     for (uint32_t w = 0; w < (1u << 25) && !mbar_try_wait(done, 0); ++w)
       if (w > 256) __nanosleep(64);
-  } else if (warp >= 2) {
+  }
+  // chains: this warp's rows of the tile, 16 at a time from (warp - 2) / 4 * 16
+  float sums[CHAINS ? 4 : 1][16];
+  if (warp >= 2) {
+    if constexpr (CHAINS) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sums[c][j] = 0.0f;
+      uint32_t tl = 0;
+      bool ok = true;
+      for (int i = 0; i < nk && ok; i += CHAIN, ++tl) {
+        const int buf = tl & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&ch_full[buf], (tl / 2) & 1));
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int c0 = ((warp - 2) >> 2) * 16 + c * 32;
+          if (c0 >= nrow) break;
+          uint32_t v[16];
+          tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)buf * (g.tmem_cols / 2) + (uint32_t)c0, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sums[c][j] += __uint_as_float(v[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ch_empty[buf]);
+      }
+      if (!ok && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    }
     if (!__all_sync(0xffffffffu, mbar_wait(done, 0)) && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
   }
   // All copies have landed and all MMAs have read them: the ring becomes the
@@ -734,16 +828,17 @@ __global__ void __launch_bounds__(S_THREADS)
   float* part = reinterpret_cast<float*>(smem);
   if (warp >= 2) {
     const int q = warp & 3;
-    for (int c0 = ((warp - 2) >> 2) * 16; c0 < nrow; c0 += 32) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int c0 = ((warp - 2) >> 2) * 16 + c * 32;
+      if (c0 >= nrow) break;
       uint32_t v[16];
-      asm volatile(
-          "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-          "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-            "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-            "=r"(v[14]), "=r"(v[15])
-          : "r"(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0));
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      if constexpr (CHAINS) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(sums[c][j]);
+      } else {
+        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
+      }
       float* p = part + c0 * 128 + q * 32 + lane;  // (rows up to NT fit)
 #pragma unroll
       for (int j = 0; j < 16; ++j) p[j * 128] = __uint_as_float(v[j]);
@@ -1108,7 +1203,7 @@ mpq_status lin_device(int* dev_out, int* sms_out) {
 // CTA keeps 4 steps.  Clusters of 8 only where they leave half of the SMs
 // free: 16 of them (256 x 1024 over 2048) find no place at once and take 18.7
 // us, clusters of 4 11.0.
-SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms) {
+SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms, bool chains) {
   SplitGeom g{};
   g.NT = rows_mn ? (o.rows <= 64 ? 64 : 128) : (int)std::min<int64_t>(128, round_up(o.rows, 16));
   const int64_t tiles = cdiv(o.cols, 128) * cdiv(o.rows, g.NT);
@@ -1122,7 +1217,7 @@ SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms) {
   // the ring must also hold the partial tile
   g.stages = std::max(g.stages, (int)cdiv(round_up(g.NT, 32) * 128 * 4, split_stage_bytes(g.NT)));
   g.tmem_cols = 32;
-  while ((int)g.tmem_cols < g.NT) g.tmem_cols *= 2;
+  while ((int)g.tmem_cols < g.NT * (chains ? 2 : 1)) g.tmem_cols *= 2;
   return g;
 }
 // What the two kernels take, in microseconds, fitted to 90 shapes of 130 to
@@ -1130,8 +1225,8 @@ SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms) {
 // where the two are near each other): a fixed part (launch, first copies, last
 // epilogue) and a part per step of 64.  256 x 512 over 2048: pair 11.7, split
 // 10.9; over 8192: 27.9 and 15.6; 1280 x 1024 over 8192: 29.9 and 35.3.
-double pair_us(const LinOut& o, int64_t KT, int pairs) {
-  const Walk w = make_walk(o.rows, o.cols, (int)std::min<int64_t>(2 * cdiv(o.rows, PT) * cdiv(o.cols, PT), pairs));
+double pair_us(const LinOut& o, int64_t KT, int pairs, bool halves) {
+  const Walk w = make_walk(o.rows, o.cols, (int)std::min<int64_t>(2 * cdiv(o.rows, PT) * cdiv(o.cols, PT), pairs), halves);
   return 6.2 + (double)KT * (0.33 * (double)cdiv(w.whole, pairs) + 0.17 * (double)cdiv(w.total - w.whole, pairs));
 }
 double split_us(int64_t tiles, const SplitGeom& g, int sms) {
@@ -1150,10 +1245,10 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
   const int64_t KT = cdiv(KC, BK);
   const int64_t big = cdiv(o.rows, PT) * cdiv(o.cols, PT);
   const int pairs = g_lin_dev[dev].pairs;
-  const SplitGeom g = split_geom(o, RN, KT, sms);
+  const SplitGeom g = split_geom(o, RN, KT, sms, std::is_same<O, float>::value);
   const int64_t at_ = cdiv(o.cols, 128), bt = cdiv(o.rows, g.NT);
   ProfScope ps_(tag, st);
-  if (pairs > 0 && o.rows > 128 && (bt > 65535 || pair_us(o, KT, pairs) <= split_us(at_ * bt, g, sms))) {
+  if (pairs > 0 && o.rows > 128 && (bt > 65535 || pair_us(o, KT, pairs, std::is_same<O, float>::value) <= split_us(at_ * bt, g, sms))) {
     CUtensorMap ta, tb, tb_half;
     MPQ_TRY(encode_box(&ta, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : 128));
     MPQ_TRY(encode_box(&tb, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
@@ -1176,7 +1271,7 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
     MPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, ta, tb, tb_half, (int)KC, o));
   } else {
     if (bt > 65535 || at_ > 65535) return fail(MPQ_ERR_INVALID_ARG, "linear: too many tiles");
-    const int smem = g.stages * split_stage_bytes(g.NT) + split_recv_bytes(g.NT, g.S) + (2 * g.stages + 2) * 8 + 16 + 1024;
+    const int smem = g.stages * split_stage_bytes(g.NT) + split_recv_bytes(g.NT, g.S) + (2 * g.stages + 6) * 8 + 16 + 1024;
     CUtensorMap ta, tb;
     MPQ_TRY(encode_box(&ta, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
     MPQ_TRY(encode_box(&tb, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : g.NT));

@@ -139,6 +139,21 @@ def test_linear_activations_and_gradients(mpq, act, rows, n, k, dtype, out):
            + tiny(dtype), "dbias")
 
 
+@pytest.mark.parametrize("rows,n,k", [(300, 1031, 1999), (777, 1032, 8192), (40, 300, 14336), (1, 200, 14336), (130, 128, 8192)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_linear_of_long_contractions_keeps_fp32(mpq, rows, n, k, dtype):
+    """fp32 results of long contractions: chains of 512 products lose at most a last bit of the accumulator at each
+    of 32 steps (2^-23 of a partial sum, half of that on average), and are then added with rounding, k / 512 times.
+    Over many results the error in the 2-norm stays near 16 half bits, 16 * 2^-24, of the partial sums' size, which
+    for independent terms is the result's; twice that is allowed."""
+    g = gen(k)
+    x = torch.randn(rows, k, generator=g, device="cuda").to(dtype)
+    w = (torch.randn(n, k, generator=g, device="cuda") / k ** 0.5).to(dtype)
+    y = mpq.linear(x, w, out_dtype=F32).double()
+    want = x.double() @ w.double().T
+    assert (y - want).norm() <= 32 * U * want.norm()
+
+
 def test_linear_takes_slices_batches_and_shared_rows(mpq):
     g = gen(7)
     x3, wide = whole(g, 3, 5, 80).to(BF), whole(g, 70, 99).to(BF)
