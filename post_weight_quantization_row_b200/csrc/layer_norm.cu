@@ -106,6 +106,28 @@ __device__ __forceinline__ Raw8<T> ln_load(const T* row, int n, int t, int G, in
   memcpy(&r, e, sizeof(r));
   return r;
 }
+// A vector on its way: as it will be used, or (PM_SHIFT) before its shift.
+template <int PM, typename T>
+using Fetched = typename std::conditional<PM != PM_ANY && (PM & PM_SHIFT), RawWindow<T>, Raw8<T>>::type;
+template <int PM, typename T>
+__device__ __forceinline__ Fetched<PM, T> ln_fetch(const T* row, int n, int t, int G, int j) {
+  if constexpr (PM != PM_ANY && (PM & PM_SHIFT)) {
+    const int c = (t + j * G) * 8;
+    if (c < n) return load_window<T>(row, c, n);
+    RawWindow<T> w;
+#pragma unroll
+    for (int i = 0; i <= (int)(sizeof(T) / 2); ++i) w.q[i] = make_uint4(0, 0, 0, 0);
+    w.halfwords = 0;
+    return w;
+  } else {
+    return ln_load<PM, T>(row, n, t, G, j);
+  }
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> ln_take(const RawWindow<T>& w) { return shift_window<T>(w); }
+template <typename T>
+__device__ __forceinline__ const Raw8<T>& ln_take(const Raw8<T>& r) { return r; }
+
 // A warp's staging for rows at any address
 template <int PM, typename T>
 struct Stage {
@@ -303,7 +325,7 @@ __global__ void __launch_bounds__(1024)
 // CTAs shares the rows, LN_PART columns each; their sums meet over distributed
 // shared memory.
 template <typename T, int NV, int PM, bool SUMS, bool CL>
-__global__ void __launch_bounds__(NV == 1 ? 128 : 512)
+__global__ void __launch_bounds__(NV == 1 && !(PM & PM_SHIFT) ? 128 : 512)
     k_ln_bwd(const __grid_constant__ LnArgs a, const T* __restrict__ dy, int64_t ldy,
              const float* __restrict__ mean, const float* __restrict__ rstd, T* __restrict__ dx,
              float* __restrict__ part) {
@@ -328,7 +350,7 @@ __global__ void __launch_bounds__(NV == 1 ? 128 : 512)
     for (int i = 0; i < 4; ++i) dw2[j].p[i] = db2[j].p[i] = 0ull;
   const int64_t step = nblocks * groups;
   int64_t row = block * groups + threadIdx.x / a.G;
-  Raw8<T> xs[NV], ds[NV];
+  Fetched<PM, T> xs[NV], ds[NV];
   float m = 0.0f, r = 0.0f;
   const auto fetch = [&](int64_t at) {  // (rows that do not exist: zeros)
     const bool live = at < a.rows;
@@ -336,8 +358,8 @@ __global__ void __launch_bounds__(NV == 1 ? 128 : 512)
     const T* yr = dy + (live ? at : 0) * ldy + c0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      xs[j] = ln_load<PM, T>(xr, live ? n : 0, t, a.G, j);
-      ds[j] = ln_load<PM, T>(yr, live ? n : 0, t, a.G, j);
+      xs[j] = ln_fetch<PM, T>(xr, live ? n : 0, t, a.G, j);
+      ds[j] = ln_fetch<PM, T>(yr, live ? n : 0, t, a.G, j);
     }
     m = live ? mean[at] : 0.0f;
     r = live ? rstd[at] : 0.0f;
@@ -354,8 +376,8 @@ __global__ void __launch_bounds__(NV == 1 ? 128 : 512)
       float w[8];
       ln_param<PM, T>(pa, pa.w, 1.0f, t, j, w);
       const F8 w2 = pairs(w);
-      xh[j] = pairs<T>(xs[j]);
-      g[j] = pairs<T>(ds[j]);
+      xh[j] = pairs<T>(ln_take<T>(xs[j]));
+      g[j] = pairs<T>(ln_take<T>(ds[j]));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // (columns that do not exist: dy = 0 there, and xh is finite)
@@ -639,7 +661,8 @@ mpq_status ln_bwd_rows(LnArgs a, const T* dy, int64_t ldy, const float* mean, co
     MPQ_CUDA(cudaLaunchKernelEx(&cfg, kernel, (const LnArgs)a, dy, ldy, mean, rstd, dx, part));
     return MPQ_OK;
   };
-  if (a.n <= 256) return go(k_ln_bwd<T, 1, PM, SUMS, false>, 1);
+  // (rows at any address hold one vector more on its way)
+  if (a.n <= (PM != PM_ANY && (PM & PM_SHIFT) ? 4096 : 256)) return go(k_ln_bwd<T, 1, PM, SUMS, false>, 1);
   if (a.n <= LN_PART) return go(k_ln_bwd<T, 2, PM, SUMS, false>, 2);
   return go(k_ln_bwd<T, 2, PM, SUMS, true>, 2);
 }

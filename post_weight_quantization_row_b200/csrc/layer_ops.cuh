@@ -211,25 +211,44 @@ __device__ __forceinline__ uint4 window16(const uint4& u, const uint4& v, int ha
 }
 // Elements at .. at + 7 of a row of n elements at any address, those past the
 // end 0.  Aligned 16-byte loads and shifts where all of them lie within the
-// row, single elements at its ends.
+// row, single elements at its ends.  In two parts, so that the loads can be in
+// flight before the shift needs them.
 template <typename T>
-__device__ __forceinline__ Raw8<T> load_row8(const T* row, int at, int n) {
+struct RawWindow {
+  uint4 q[sizeof(T) / 2 + 1];
+  int halfwords;  // how far into q the elements begin
+};
+template <typename T>
+__device__ __forceinline__ RawWindow<T> load_window(const T* row, int at, int n) {
   const T* p = row + at;
   const uintptr_t a = (uintptr_t)p;
-  if ((a & 15) == 0) return load_raw<T>(p, n - at, true);
-  constexpr int V = 16 / (int)sizeof(T);  // elements of a 16-byte vector
+  constexpr int V = 16 / (int)sizeof(T);           // elements of a 16-byte vector
   const int off = (int)(a & 15) / (int)sizeof(T);  // elements past the boundary
-  if (at < off || at - off + 8 + V > n) return load_raw<T>(p, n - at, false);
-  const uint4* q = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
-  Raw8<T> r;
-  uint4 u = q[0];
+  RawWindow<T> w;
+  if (off && at >= off && at - off + 8 + V <= n) {
+    const uint4* q = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
 #pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) {
-    const uint4 v = q[i + 1];
-    r.q[i] = window16(u, v, (int)(a & 15) >> 1);
-    u = v;
+    for (int i = 0; i <= (int)(sizeof(T) / 2); ++i) w.q[i] = q[i];
+    w.halfwords = (int)(a & 15) >> 1;
+  } else {
+    const Raw8<T> r = load_raw<T>(p, n - at, off == 0);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w.q[i] = r.q[i];
+    w.q[sizeof(T) / 2] = make_uint4(0, 0, 0, 0);
+    w.halfwords = 0;
   }
+  return w;
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> shift_window(const RawWindow<T>& w) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.q[i] = window16(w.q[i], w.q[i + 1], w.halfwords);
   return r;
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_row8(const T* row, int at, int n) {
+  return shift_window<T>(load_window<T>(row, at, n));
 }
 // Stores a warp's 8 elements a lane, 256 neighbours of a row of which `total`
 // exist, at any address: through `stage` (shared memory of the warp, 256
