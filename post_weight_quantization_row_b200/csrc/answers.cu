@@ -18,6 +18,12 @@
 // so only their columns are read again, from L2.  The candidates are ranked
 // by counting.  The order is (logit descending, id ascending) throughout: a
 // total order, so the result does not depend on the order of any atomics.
+//
+// What bounds them: HBM by the bytes, and before it the issue of an exponential
+// and its arithmetic per element.  At 1024 rows of 131072 bf16 logits (268 MB):
+// token_logprobs without alternatives 58 us (4.6 TB/s), with 20 alternatives 77
+// (3.5 TB/s; 61% of the issue slots); topk_distill, which reads the row twice
+// and writes the gradient, 125 us against 82 for the bytes read once.
 #include <algorithm>
 #include <type_traits>
 
@@ -68,6 +74,18 @@ struct Row {
     return r;
   }
 };
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> encode(const float (&x)[8]) {
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 4) {
+    memcpy(&r, x, sizeof(r));
+  } else {
+    const T* t = nullptr;
+    r.q[0] = make_uint4(pack2(x[0], x[1], t), pack2(x[2], x[3], t), pack2(x[4], x[5], t), pack2(x[6], x[7], t));
+  }
+  return r;
+}
 
 struct Soft {  // the running softmax: scaled maximum, sums
   float m, s, u;
@@ -613,7 +631,10 @@ __global__ void __launch_bounds__(AT, 1024 / AT) k_topk_distill(const __grid_con
     };
     constexpr int U = sizeof(T) == 4 ? 2 : 4;
     const uint64_t k2 = f2_pack(a.k, a.k), m2 = f2_pack(-st.a.m, -st.a.m), c2 = f2_pack(cs, cs);
-    for (int g0 = lo2 + (int)threadIdx.x; g0 < hi2; g0 += AT * U) {
+    // from the end of the row, which L2 got last (132 us become 128 at 1024 rows
+    // of 131072 bf16; stores that leave L2 to the logits: 125)
+    for (int tile = (hi2 - lo2 + AT * U - 1) / (AT * U) - 1; tile >= 0; --tile) {
+      const int g0 = lo2 + tile * (AT * U) + (int)threadIdx.x;
       Raw8<T> raw[U];
 #pragma unroll
       for (int j = 0; j < U; ++j)
@@ -637,7 +658,10 @@ __global__ void __launch_bounds__(AT, 1024 / AT) k_topk_distill(const __grid_con
         }
         const int col = dst.col(g);
         if (col >= 0 && col + 8 <= a.v) {
-          store_vec<8>(out + col, x, true);
+          Raw8<T> y = encode<T>(x);
+          uint4* d = reinterpret_cast<uint4*>(out + col);
+#pragma unroll
+          for (int i = 0; i < (int)(sizeof(T) / 2); ++i) __stcs(d + i, y.q[i]);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -715,7 +739,9 @@ mpq_status run_logprobs(const LogprobArgs& a, cudaStream_t st) {
 template <typename T>
 mpq_status run_distill(const DistillArgs& a, cudaStream_t st) {
   // the second reading of a row should find it in L2 (1024 rows of 131072
-  // bf16: 132 us with 512 threads, 145 with 256; 4096 rows of 32000: 139, 122)
+  // bf16, 20 entries, in row order: 132 us with 512 threads, 144 with 256; from
+  // the row's end with streaming stores 125; 4096 rows of 32000: 139 with 512,
+  // 121 with 256.  Clusters of 2 and 4 CTAs a row: 137 to 181, 169 to 450)
   const bool large = a.dlogits && large_rows<T>(a.C, a.v);
   if (large) return launch_rows(k_topk_distill<512, T, false>, k_topk_distill<512, T, true>, a, 512, st, "k_topk_distill");
   return launch_rows(k_topk_distill<256, T, false>, k_topk_distill<256, T, true>, a, 256, st, "k_topk_distill");
