@@ -422,7 +422,9 @@ typedef enum {
  *   0 <= rows <= 2^23, 1 <= n, k <= 2^22.  A workspace is needed only where x
  *   or weight has a base or a row stride that is no multiple of 16 bytes, or
  *   rows that overlap.
- * The products run on the tensor cores with fp32 accumulation. */
+ * The products run on the tensor cores with fp32 accumulation; for an MPQ_F32
+ * y the accumulator is added up every 512 products, which rounds where the
+ * tensor cores truncate.  Activations take their limits at +-inf (0 at -inf). */
 MPQ_API int64_t mpq_linear_workspace_bytes(const void* x, int64_t ldx, const void* weight, int64_t ldw,
                                            int64_t rows, int64_t n, int64_t k);
 MPQ_API mpq_status mpq_linear(const void* x, int64_t ldx, const void* weight, int64_t ldw, int64_t rows,
@@ -437,7 +439,8 @@ MPQ_API mpq_status mpq_linear(const void* x, int64_t ldx, const void* weight, in
  *   solved weights frozen, dweight is).  The residual's gradient is dy.
  *   preact: rows x n of dtype, as mpq_linear wrote it; not read (may be NULL)
  *   for MPQ_ACT_NONE.  x is not read without dweight, weight not without dx.
- *   dz is rounded to dtype for the tensor cores; dbias sums it unrounded.
+ *   dz is rounded to dtype for the tensor cores (in MPQ_F16 what passes 65504
+ *   becomes infinite, as dy itself would); dbias sums it unrounded.
  *   rows = 0 leaves zeros in dweight and dbias. */
 MPQ_API int64_t mpq_linear_backward_workspace_bytes(const void* dy, int64_t ldy, const void* x, int64_t ldx,
                                                     const void* weight, int64_t ldw, int64_t rows, int64_t n,

@@ -193,6 +193,24 @@ def test_linear_keeps_infinities_and_nans_to_their_rows(mpq):
         assert torch.equal(y[1:2], (x[1:2].double() @ w.double().T).to(BF)) and torch.isfinite(y[3:]).all()
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("rows", [1, 40, 300])  # a kernel each
+def test_linear_activations_at_infinity(mpq, act, rows):
+    """z = +inf, -inf, NaN: the limits inf, 0 and NaN, and slopes 1, 0 and NaN."""
+    x = torch.ones(rows, 64, device="cuda", dtype=BF)
+    w = torch.zeros(16, 64, device="cuda", dtype=BF)
+    w[0, 3], w[1, 3], w[2, 3], w[3, 3], w[4, 3] = math.inf, -math.inf, math.nan, 1e30, -1e30
+    want = torch.tensor([math.inf, 0, math.nan, w[3, 3].item()] + [0] * 12, device="cuda", dtype=BF).expand(rows, 16)
+    y, z = mpq.linear(x, w, activation=act, preact=True)
+    assert torch.equal(torch.nan_to_num(y, nan=7.0), torch.nan_to_num(want, nan=7.0))
+    d = mpq.linear_backward(torch.ones_like(y), None, None, z, activation=act, dx=False, dweight=False,
+                            bias_dtype=torch.float32)["dbias"]
+    # slopes are taken at |z| <= 30: 29 e^-30 = 2.8e-12 is left of silu's there; a rounding or two of 1 + e^-30
+    assert torch.isnan(d[2])
+    torch.testing.assert_close(d[[0, 1, 3, 4]], torch.tensor([rows, 0, rows, 0], device="cuda", dtype=F32),
+                               rtol=2**-21, atol=3e-12 * rows)
+
+
 # ------------------------------------------------------------- layer norm --
 LN = [(1, 1), (1, 16), (3, 5), (33, 64), (700, 17), (9, 256), (130, 257), (5, 1000), (300, 1024), (64, 4096), (1, 8192),
       (7, 8200), (3, 16384), (2, 16400), (5, 32768), (3, 40001)]
