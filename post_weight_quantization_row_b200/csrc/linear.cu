@@ -14,8 +14,8 @@
 //  - k_lin_split: one 128 x (16..128) tile per cluster of S CTAs, each taking
 //    1/S of the contraction; the partial tiles are joined over distributed
 //    shared memory in a fixed order.  For few rows and for small outputs.
-// Up to GEMV_ROWS rows of x W^T need no tensor cores: k_lin_gemv reads W once
-// with a warp per row of it (and any alignment).
+// One row of x W^T, and two of small or unaligned W, need no tensor cores:
+// k_lin_gemv reads W once with a warp per row of it (and any alignment).
 // The epilogue adds the bias, applies the activation, adds the residual and
 // rounds once, in fp32 before that.
 //
@@ -937,8 +937,6 @@ __global__ void __launch_bounds__(S_THREADS)
 // y = x W^T for one or two rows of x, bound by the read of W: WPR warps share a
 // row of W, 16 bytes a lane and load, four loads in flight; the sums meet by
 // shuffles and, for WPR > 1, in shared memory.  x comes from L1.
-// Two rows, the most that the loads of W leave room for: from three on the
-// split kernel reads W once for all.
 constexpr int GEMV_ROWS = 2, GEMV_WARPS = 8;
 template <typename T, typename O, int MR, bool VEC>
 __global__ void __launch_bounds__(GEMV_WARPS * 32, 4)
@@ -1321,11 +1319,20 @@ mpq_status check_dims(const char* who, int64_t rows, int64_t n, int64_t k, int32
   return MPQ_OK;
 }
 
-bool use_gemv(int64_t rows) { return rows <= GEMV_ROWS; }
+// Two rows double the arithmetic per byte of W, which then sets the pace where W
+// is large: 4096 -> 4096 takes 12.1 us (the split kernel 10.1), 4096 -> 14336
+// 30.6 (24.3), but 8192 -> 512 4.9 (9.5) and 1024 -> 1024 3.5 (6.2).  One row: 8.9
+// (10.4), 23.9 (24.3), and 1024 -> 8192 6.9 (8.1).  Without packing W first only
+// this kernel reads rows at any address.
+bool use_gemv(const Operand& x, const Operand& w) {
+  if (x.rows <= 1) return true;
+  return x.rows <= GEMV_ROWS && (w.rows * w.inner <= (1 << 23) || !tma_ok(x.p, x.inner, x.rows, x.ld) ||
+                                 !tma_ok(w.p, w.inner, w.rows, w.ld));
+}
 
 template <typename T, typename O>
 mpq_status linear_fwd(Operand x, Operand w, const LinOut& o, char* ws, cudaStream_t st) {
-  if (use_gemv(x.rows)) {
+  if (use_gemv(x, w)) {
     // a warp per row of W fills the device from 24 warps an SM on; below that
     // more warps share a row, as long as each has 512 elements
     int wpr = 1;
@@ -1424,7 +1431,7 @@ using namespace mpq;
 
 extern "C" int64_t mpq_linear_workspace_bytes(const void* x, int64_t ldx, const void* weight, int64_t ldw,
                                               int64_t rows, int64_t n, int64_t k) {
-  if (rows < 1 || n < 1 || k < 1 || use_gemv(rows)) return 0;
+  if (rows < 1 || n < 1 || k < 1 || use_gemv({x, k, rows, ldx}, {weight, k, n, ldw})) return 0;
   return (tma_ok(x, k, rows, ldx) ? 0 : packed_bytes(k, rows)) + (tma_ok(weight, k, n, ldw) ? 0 : packed_bytes(k, n));
 }
 
