@@ -63,8 +63,8 @@ def act64(z, name):
 # rows, n, k: one token to several tiles; sizes that no tile, vector or
 # swizzled box divides; contractions of one element and of many steps
 SHAPES = [(1, 1, 1), (1, 4096, 512), (2, 129, 65), (2, 2056, 4104), (2, 2050, 4101), (5, 8, 4104),
-          (16, 256, 64), (17, 130, 1000), (63, 1000, 333), (64, 136, 2048),
-          (128, 512, 200), (129, 257, 72), (300, 384, 520), (777, 130, 1001), (1100, 1032, 264), (2048, 2000, 129), (3000, 2500, 64), (4097, 1304, 96)]
+          (16, 256, 64), (17, 130, 1000), (63, 1000, 333), (64, 136, 2048), (128, 512, 200), (129, 257, 72),
+          (300, 384, 520), (777, 130, 1001), (1100, 1032, 264), (2048, 2000, 129), (3000, 2500, 64), (4097, 1304, 96)]
 
 
 @pytest.mark.parametrize("rows,n,k", SHAPES)
