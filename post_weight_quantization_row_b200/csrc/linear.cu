@@ -28,10 +28,13 @@
 //
 // The tensor cores' accumulator drops what falls below its last bit instead of
 // rounding it, so a long chain of products drifts towards zero: 2.4e-6 of the
-// result over a contraction of 2000, 8.7e-6 over 14336.  Results of 16 bits
-// hide that (their own half step is 5e-4 or 4e-3); for fp32 results a chain
-// ends after CHAIN steps and the chains are added, rounded, in the epilogue's
-// registers, which keeps the error below 1e-6 at any length.
+// result over a contraction of 2000, 8.7e-6 over 14336, and for terms of one
+// sign 7.8e-4 over 2^20, more than half a step of fp16.  So a chain ends after
+// chain_steps<O>() steps and the chains are added, rounded, in the epilogue's
+// registers: after 512 products for fp32 results, which keeps their error below
+// 1e-6 at any length, and after 4096 for 16-bit ones: 256 last bits at most,
+// 3e-5 (measured: 7e-6 over 14336, 2e-5 for terms of one sign), where their half
+// step is 5e-4 or 4e-3.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -207,7 +210,13 @@ __device__ __forceinline__ void act_grad8(F8& g, const F8& z, int act) {
 // ------------------------------------------------------------- the operand --
 constexpr int BK = 64;              // contraction per stage
 constexpr int BOX = 64 * 64 * 2;    // bytes of a 64 x 64 box (8 KiB)
-constexpr int CHAIN = 8;            // steps accumulated at a stretch for fp32 results
+// Steps accumulated at a stretch: 512 products for fp32 results, 4096 for 16-bit
+// ones.  A second chain costs 16-bit results 3 us of code that runs for the
+// first time (1024 x 4096 -> 4096, GELU: 37.4 us with chains of 2048, 34.5 with
+// 4096); 4096 x 14336 -> 4096 takes 302 us against 300 in one chain, 307 with
+// chains of 2048 and 326 with 512.
+template <typename O>
+__host__ __device__ constexpr int chain_steps() { return sizeof(O) == 4 ? 8 : 64; }
 
 // Operand tiles of 64 (contraction) x 64 .. 128, with 128-byte swizzle.
 // K-major (rows of 64 contraction elements): 8 rows are 1024 B apart; 16
@@ -326,7 +335,14 @@ constexpr int PT = 256;                    // tile: 256 rows x 256 columns
 constexpr int P_RING = 6 * 2 * 128 * BK * 2;  // 6 stages of 128 rows of A and 128 of B per CTA,
 constexpr int P_STAGES = 8;                   // or 8 of 128 and 64 (128-column tiles only)
 constexpr int P_EPI = 8;                   // epilogue warps
-constexpr int P_THREADS = 32 * (3 + P_EPI);
+// Three warpgroups: copies and MMAs (a warp is idle), and two of epilogue warps,
+// which take over registers for their part of a tile's sums, 128 a thread.
+constexpr int P_THREADS = 32 * (4 + P_EPI);
+// (Each role sets its own share in its own branch: where branches of different
+// shares meet, the compiler keeps to the smaller one.)
+constexpr int P_REGS = 168, P_REGS_ISSUE = 72, P_REGS_EPI = 216;
+static_assert(P_THREADS * P_REGS <= 65536 && 128 * P_REGS_ISSUE + 256 * P_REGS_EPI <= P_THREADS * P_REGS,
+              "a block moves the registers that it was launched with");
 constexpr int P_SMEM = P_RING + P_EPI * 4096 + 1024 + 256;
 static_assert(P_SMEM <= 232448, "pair kernel's shared memory");
 
@@ -336,13 +352,12 @@ static_assert(P_SMEM <= 232448, "pair kernel's shared memory");
 struct Walk {
   int mt, nt, whole, total;
 };
-// (halves: 128-column tiles only, whose sums fit the epilogue's registers.)
-__host__ __device__ inline Walk make_walk(int rows, int cols, int workers, bool halves) {
+__host__ __device__ inline Walk make_walk(int rows, int cols, int workers) {
   Walk w;
   w.mt = (rows + PT - 1) / PT;
   w.nt = (cols + PT - 1) / PT;
   const int t = w.mt * w.nt, left = t % workers;
-  w.whole = halves ? 0 : 2 * left <= workers ? t - left : t;
+  w.whole = 2 * left <= workers ? t - left : t;
   w.total = w.whole + 2 * (t - w.whole);
   return w;
 }
@@ -383,8 +398,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // rank 0 issues the pair's MMAs
   const int worker = (int)cluster_id_x(), nworkers = (int)(gridDim.x / 2);
-  constexpr bool CHAINS = std::is_same<O, float>::value;
-  const Walk walk = make_walk(o.rows, o.cols, nworkers, CHAINS);
+  constexpr int CHAIN = chain_steps<O>();
+  const Walk walk = make_walk(o.rows, o.cols, nworkers);
   const int KT = (KC + BK - 1) / BK;
   const int stages = walk.whole ? 6 : 8, stage = walk.whole ? P_RING / 6 : P_RING / 8;
 
@@ -417,6 +432,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   const uint32_t full_r0 = map_to_rank(smem_u32(full), 0);
   const uint32_t tm_empty_r0 = map_to_rank(smem_u32(tm_empty), 0);
 
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P_REGS_ISSUE));
   if ((warp == 0 || warp == 2) && lane == 0) {
     // ------------------------------------------------- producers: A and B
     const bool is_a = warp == 0;
@@ -461,15 +477,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t ID_W = lin_idesc<T, A_MN, B_MN>(256, PT), ID_N = lin_idesc<T, A_MN, B_MN>(256, PT / 2);
     const uint64_t da0 = op_desc<A_MN>(smem_u32(smem)), db0 = op_desc<B_MN>(smem_u32(smem) + 128 * BK * 2);
-    const int CH = CHAINS ? CHAIN : KT;
     uint32_t tl = 0;  // accumulators filled
     int s = 0;
     uint32_t phase = 0;
     bool ok = true, ready = false;
     for (int t = worker; t < walk.total; t += nworkers) {
       const uint32_t idesc = t < walk.whole ? ID_W : ID_N;
-      for (int k0 = 0; k0 < KT; k0 += CH, ++tl) {  // a chain into an accumulator
-        const int buf = tl & 1, n = min(CH, KT - k0);
+      for (int k0 = 0; k0 < KT; k0 += CHAIN, ++tl) {  // a chain into an accumulator
+        const int buf = tl & 1, n = min(CHAIN, KT - k0);
         // elect.sync needs every lane, so a wait that runs out ends no loop: its
         // lane waits no more, and the result is reported as undefined
         if (ok && tl >= 2) ok = mbar_wait_cl(&tm_empty[buf], (tl / 2 - 1) & 1);
@@ -500,17 +515,19 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     for (uint32_t q = (tl > 2 ? tl - 2 : 0); q < tl; ++q)  // MMAs finish before TMEM is freed
       for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&tm_full[q & 1], (q / 2) & 1); ++i)
         if (i > 256) __nanosleep(64);
-  } else if (warp >= 3) {
+  } else if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P_REGS_EPI));
     // -------------------------------------------------------------- epilogue
-    // two warps per TMEM lane quadrant, alternating over 32-column chunks.  A
-    // chunk goes through a swizzled 32 x 32 fp32 staging tile, which turns
-    // the lane-per-row layout into 8 consecutive columns per lane.
-    const int q = warp & 3, side = (warp - 3) >> 2;
-    float4* stg = reinterpret_cast<float4*>(stg_all + (warp - 3) * 4096);
+    // two warps per TMEM lane quadrant, alternating over 32-column chunks: up to
+    // four each, whose chains are added up here.  Then a chunk goes through a
+    // swizzled 32 x 32 fp32 staging tile, which turns the lane-per-row layout
+    // into 8 consecutive columns per lane.
+    const int q = warp & 3, side = (warp - 4) >> 2;
+    float4* stg = reinterpret_cast<float4*>(stg_all + (warp - 4) * 4096);
     const int c8 = (lane & 3) * 8, r8 = lane >> 2;
     const bool wide = o.out_vec && (!o.residual || o.res_vec);
     uint32_t tl = 0;
-    for (int t = worker; t < walk.total; t += nworkers, ++tl) {
+    for (int t = worker; t < walk.total; t += nworkers) {
       int m0, n0, wn;
       walk_tile(walk, t, m0, n0, wn);
       const int row0 = m0 + (int)rank * 128 + q * 32;
@@ -521,38 +538,53 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(rl + min(c + 31, o.cols - 1)));
         }
       }
-      // CHAINS: the chains of this warp's two 32-column chunks, added up
-      float sum0[CHAINS ? 32 : 1], sum1[CHAINS ? 32 : 1];
+      // Chains of this warp's two or four chunks: all of them for fp32 results,
+      // those before the last for 16-bit ones, which are often a single one.
+      constexpr bool ALL = sizeof(O) == 4;
+      float sum[4][32];
+      const auto add = [&](int c, uint32_t at) {
+        uint32_t a[32];
+        tmem_ld32(at + 64u * (uint32_t)c, a);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(a[i]);
+      };
+      const bool chains = ALL || KT > CHAIN;
       bool ok = true;
-      if constexpr (CHAINS) {
-        for (int k = 0; k < KT && ok; k += CHAIN) {
+      if (chains) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[0][i] = sum[1][i] = 0.0f;
+        if (wn == PT) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[2][i] = sum[3][i] = 0.0f;
+        }
+        for (int k = ALL ? 0 : CHAIN; k < KT && ok; k += CHAIN, ++tl) {
           const int buf = tl & 1;
           ok = __all_sync(0xffffffffu, mbar_wait_cl(&tm_full[buf], (tl / 2) & 1));
           tc_fence_after();
           const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * PT + side * 32);
-          uint32_t a[32], b[32];
-          tmem_ld32(tb, a);
-          tmem_ld32(tb + 64, b);
+          add(0, tb);
+          add(1, tb);
+          if (wn == PT) {
+            add(2, tb);
+            add(3, tb);
+          }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            sum0[i] = (k ? sum0[i] : 0.0f) + __uint_as_float(a[i]);
-            sum1[i] = (k ? sum1[i] : 0.0f) + __uint_as_float(b[i]);
-          }
-          if (k + CHAIN < KT) ++tl;
+          if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);  // read: hand the accumulator back
         }
-      } else {
-        ok = __all_sync(0xffffffffu, mbar_wait_cl(&tm_full[tl & 1], (tl / 2) & 1));
+      }
+      const int buf = tl & 1;  // (not ALL: the last chain's)
+      if constexpr (!ALL) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cl(&tm_full[buf], (tl / 2) & 1));
         tc_fence_after();
+        ++tl;
       }
       if (!ok) {
         if (lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
         break;
       }
-      const int buf = tl & 1;
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)buf * PT;
+#pragma unroll 1
       for (int c0 = side * 32; c0 < wn; c0 += 64) {
         const int left = o.cols - (n0 + c0), top = o.rows - row0;  // columns and rows from this chunk on
         const bool inside = wide && left >= 32 && top >= 32;
@@ -570,10 +602,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           }
         }
         uint32_t v[32];
-        if constexpr (CHAINS) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(c0 < 64 ? sum0[i] : sum1[i]);
-        } else {
+        if constexpr (!ALL) {
           tmem_ld32(tbase + (uint32_t)c0, v);
           if (c0 + 64 >= wn) {  // this warp's part is read: hand the accumulator back
             tc_fence_before();
@@ -581,6 +610,16 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             if (lane == 0) mbar_arrive_cl(tm_empty_r0 + 8u * (uint32_t)buf);
           }
         }
+        // (the loop is not unrolled: selects)
+        const auto take = [&](const float (&even)[32], const float (&odd)[32]) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float w = c0 & 64 ? odd[i] : even[i];
+            v[i] = __float_as_uint(ALL ? w : __uint_as_float(v[i]) + w);
+          }
+        };
+        if (chains && c0 < 128) take(sum[0], sum[1]);
+        else if (chains) take(sum[2], sum[3]);
         if (left <= 0 || top <= 0) continue;
         __syncwarp();
 #pragma unroll
@@ -664,6 +703,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 // fills the 128 TMEM lanes, the one with its rows (the tokens) the NT columns
 // of the accumulator, so few rows waste no tensor work.
 constexpr int S_THREADS = 320;  // copies, MMAs, 8 epilogue warps
+constexpr int S_NARROW = 32;    // rows of a tile of which two CTAs fit on an SM
 
 struct SplitGeom {
   int NT;      // rows of the output per tile (accumulator columns)
@@ -671,6 +711,7 @@ struct SplitGeom {
   int S;       // CTAs per cluster, each with its share of the contraction
   int KT;      // contraction steps in all
   uint32_t tmem_cols;
+  bool chains;
 };
 __host__ __device__ inline int split_stage_bytes(int NT) { return 128 * BK * 2 + NT * BK * 2; }
 __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&v)[16]) {
@@ -688,8 +729,10 @@ __host__ __device__ inline int split_share(int rows, int S) { return ((rows * 12
 // Shared memory behind the ring for the partial tiles of S > 1 CTAs
 __host__ __device__ inline int split_recv_bytes(int NT, int S) { return S > 1 ? S * split_share(NT, S) * 4 : 0; }
 
-template <typename T, typename O, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(S_THREADS)
+// CHAINS: the chains of a CTA's contraction are added up in registers, NC blocks
+// of 16 rows a warp (one for tiles of up to S_NARROW rows); else it is one chain.
+template <typename T, typename O, bool A_MN, bool B_MN, bool CHAINS, int NC>
+__global__ void __launch_bounds__(S_THREADS, NC == 1 || !CHAINS ? 2 : 1)
     k_lin_split(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const __grid_constant__ SplitGeom g, const __grid_constant__ LinOut o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -703,7 +746,6 @@ __global__ void __launch_bounds__(S_THREADS)
   uint64_t* ch_full = arrived + 1;  // chains (fp32 results): two accumulators in turn
   uint64_t* ch_empty = ch_full + 2;
   uint32_t* tmem_slot = (uint32_t*)(ch_empty + 2);
-  constexpr bool CHAINS = std::is_same<O, float>::value;
 
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = g.S > 1 ? (int)cluster_ctarank() : 0;
@@ -767,7 +809,7 @@ __global__ void __launch_bounds__(S_THREADS)
   } else if (warp == 1) {
     const uint32_t idesc = lin_idesc<T, A_MN, B_MN>(128, g.NT);
     const uint64_t da0 = op_desc<A_MN>(smem_u32(smem)), db0 = op_desc<B_MN>(smem_u32(smem) + 128 * BK * 2);
-    const int CH = CHAINS ? CHAIN : nk;
+    const int CH = CHAINS ? chain_steps<O>() : nk;
     int s = 0;
     uint32_t phase = 0, tl = 0;
     bool ok = true, ready = false;
@@ -807,21 +849,21 @@ __global__ void __launch_bounds__(S_THREADS)
       if (w > 256) __nanosleep(64);
   }
   // chains: this warp's rows of the tile, 16 at a time from (warp - 2) / 4 * 16
-  float sums[CHAINS ? 4 : 1][16];
+  float sums[CHAINS ? NC : 1][16];
   if (warp >= 2) {
     if constexpr (CHAINS) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int j = 0; j < 16; ++j) sums[c][j] = 0.0f;
       uint32_t tl = 0;
       bool ok = true;
-      for (int i = 0; i < nk && ok; i += CHAIN, ++tl) {
+      for (int i = 0; i < nk && ok; i += chain_steps<O>(), ++tl) {
         const int buf = tl & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(&ch_full[buf], (tl / 2) & 1));
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < NC; ++c) {
           const int c0 = ((warp - 2) >> 2) * 16 + c * 32;
           if (c0 >= nrow) break;
           uint32_t v[16];
@@ -846,7 +888,7 @@ __global__ void __launch_bounds__(S_THREADS)
   if (warp >= 2) {
     const int q = warp & 3;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < NC; ++c) {
       const int c0 = ((warp - 2) >> 2) * 16 + c * 32;
       if (c0 >= nrow) break;
       uint32_t v[16];
@@ -1159,13 +1201,37 @@ mpq_status pack(Operand* a, void* dst_a, Operand* b, void* dst_b, cudaStream_t s
   return check_launch("k_lin_pack");
 }
 
+// The split kernel of a product: chains where a CTA's part of the contraction is
+// longer than one (always for fp32 results, whose chains are short).
+template <typename T, typename O, bool RN, bool CN>
+auto split_kernel(bool chains, int NT) {
+  auto k = k_lin_split<T, O, CN, RN, true, 4>;
+  if constexpr (!RN)
+    if (chains && NT <= S_NARROW) return k_lin_split<T, O, CN, RN, true, 1>;
+  if constexpr (sizeof(O) == 2)
+    if (!chains) return k_lin_split<T, O, CN, RN, false, 4>;
+  return k;
+}
+
+// Its epilogue warps wait for the registers that the issuing warps give up: a
+// build that launched the block with fewer than it moves would wait for good.
+template <typename K>
+mpq_status pair_attrs(K kernel) {
+  cudaFuncAttributes a{};
+  MPQ_CUDA(cudaFuncGetAttributes(&a, kernel));
+  if (a.numRegs != P_REGS)
+    return fail(MPQ_ERR_CUDA, "linear: the pair kernel was built with " + std::to_string(a.numRegs) + " registers");
+  MPQ_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
+  return MPQ_OK;
+}
 template <typename T, typename O, bool RN, bool CN>
 mpq_status set_attrs() {
-  MPQ_CUDA(cudaFuncSetAttribute(k_lin_pair<T, O, RN, CN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
-  if constexpr (!RN && !CN)
-    MPQ_CUDA(cudaFuncSetAttribute(k_lin_pair<T, O, RN, CN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
-  MPQ_CUDA(cudaFuncSetAttribute(k_lin_split<T, O, CN, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                220 * 1024));
+  MPQ_TRY(pair_attrs(k_lin_pair<T, O, RN, CN, false>));
+  if constexpr (!RN && !CN) MPQ_TRY(pair_attrs(k_lin_pair<T, O, RN, CN, true>));
+  for (const bool chains : {false, true})
+    for (const int NT : {S_NARROW, 128})
+      MPQ_CUDA(cudaFuncSetAttribute(split_kernel<T, O, RN, CN>(chains, NT), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    220 * 1024));
   return MPQ_OK;
 }
 
@@ -1220,11 +1286,11 @@ mpq_status lin_device(int* dev_out, int* sms_out) {
 // CTA keeps 4 steps.  Clusters of 8 only where they leave half of the SMs
 // free: 16 of them (256 x 1024 over 2048) find no place at once and take 18.7
 // us, clusters of 4 11.0.
-SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms, bool chains) {
+SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms, int chain) {
   SplitGeom g{};
   g.NT = rows_mn ? (o.rows <= 64 ? 64 : 128) : (int)std::min<int64_t>(128, round_up(o.rows, 16));
   const int64_t tiles = cdiv(o.cols, 128) * cdiv(o.rows, g.NT);
-  const int per_sm = g.NT <= 32 ? 2 : 1;
+  const int per_sm = g.NT <= S_NARROW ? 2 : 1;
   g.S = 1;
   while (g.S < 4 && tiles * g.S * 2 <= per_sm * sms && KT >= 4 * g.S) g.S *= 2;
   if (g.S == 4 && tiles * 8 <= sms / 2 && KT >= 16) g.S = 8;
@@ -1233,8 +1299,9 @@ SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms, bool ch
   g.stages = (int)std::min<int64_t>(std::min(budget / split_stage_bytes(g.NT), 12), std::max<int64_t>(cdiv(KT, g.S), 1));
   // the ring must also hold the partial tile
   g.stages = std::max(g.stages, (int)cdiv(round_up(g.NT, 32) * 128 * 4, split_stage_bytes(g.NT)));
+  g.chains = chain <= chain_steps<float>() || cdiv(KT, g.S) > chain;
   g.tmem_cols = 32;
-  while ((int)g.tmem_cols < g.NT * (chains ? 2 : 1)) g.tmem_cols *= 2;
+  while ((int)g.tmem_cols < g.NT * (g.chains ? 2 : 1)) g.tmem_cols *= 2;
   return g;
 }
 // What the two kernels take, in microseconds, fitted to 90 shapes of 130 to
@@ -1242,8 +1309,8 @@ SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms, bool ch
 // where the two are near each other): a fixed part (launch, first copies, last
 // epilogue) and a part per step of 64.  256 x 512 over 2048: pair 11.7, split
 // 10.9; over 8192: 27.9 and 15.6; 1280 x 1024 over 8192: 29.9 and 35.3.
-double pair_us(const LinOut& o, int64_t KT, int pairs, bool halves) {
-  const Walk w = make_walk(o.rows, o.cols, (int)std::min<int64_t>(2 * cdiv(o.rows, PT) * cdiv(o.cols, PT), pairs), halves);
+double pair_us(const LinOut& o, int64_t KT, int pairs) {
+  const Walk w = make_walk(o.rows, o.cols, (int)std::min<int64_t>(2 * cdiv(o.rows, PT) * cdiv(o.cols, PT), pairs));
   return 6.2 + (double)KT * (0.33 * (double)cdiv(w.whole, pairs) + 0.17 * (double)cdiv(w.total - w.whole, pairs));
 }
 double split_us(int64_t tiles, const SplitGeom& g, int sms) {
@@ -1262,10 +1329,10 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
   const int64_t KT = cdiv(KC, BK);
   const int64_t big = cdiv(o.rows, PT) * cdiv(o.cols, PT);
   const int pairs = g_lin_dev[dev].pairs;
-  const SplitGeom g = split_geom(o, RN, KT, sms, std::is_same<O, float>::value);
+  const SplitGeom g = split_geom(o, RN, KT, sms, chain_steps<O>());
   const int64_t at_ = cdiv(o.cols, 128), bt = cdiv(o.rows, g.NT);
   ProfScope ps_(tag, st);
-  if (pairs > 0 && o.rows > 128 && (bt > 65535 || pair_us(o, KT, pairs, std::is_same<O, float>::value) <= split_us(at_ * bt, g, sms))) {
+  if (pairs > 0 && o.rows > 128 && (bt > 65535 || pair_us(o, KT, pairs) <= split_us(at_ * bt, g, sms))) {
     CUtensorMap ta, tb, tb_half;
     MPQ_TRY(encode_box(&ta, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : 128));
     MPQ_TRY(encode_box(&tb, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
@@ -1304,7 +1371,7 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    MPQ_CUDA(cudaLaunchKernelEx(&cfg, k_lin_split<T, O, CN, RN>, ta, tb, g, o));
+    MPQ_CUDA(cudaLaunchKernelEx(&cfg, split_kernel<T, O, RN, CN>(g.chains, g.NT), ta, tb, g, o));
   }
   count_launch();
   return check_launch(tag);
