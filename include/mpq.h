@@ -412,6 +412,7 @@ typedef enum {
   MPQ_ACT_GELU_TANH = 3, /* z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))   */
   MPQ_ACT_SILU = 4       /* z / (1 + e^-z)                                    */
 } mpq_act;
+#define MPQ_DZ_ROUNDED 0x100 /* with an mpq_act, for mpq_linear_backward */
 
 /* y = act(z) + residual, z = x W^T + bias.
  *   x: rows x k, weight: n x k (one row per output, the layout of w_hat),
@@ -439,8 +440,12 @@ MPQ_API mpq_status mpq_linear(const void* x, int64_t ldx, const void* weight, in
  *   solved weights frozen, dweight is).  The residual's gradient is dy.
  *   preact: rows x n of dtype, as mpq_linear wrote it; not read (may be NULL)
  *   for MPQ_ACT_NONE.  x is not read without dweight, weight not without dx.
- *   dz is rounded to dtype for the tensor cores (in MPQ_F16 what passes 65504
- *   becomes infinite, as dy itself would); dbias sums it unrounded.
+ *   dz of a smooth activation (gelu, gelu_tanh, silu) goes to the tensor cores
+ *   in two parts of dtype that hold it to 2^-16 (MPQ_BF16) or 2^-22 (MPQ_F16,
+ *   and 2^-25 absolute), which takes twice the products.  With act |
+ *   MPQ_DZ_ROUNDED it is rounded to dtype (half a step; in MPQ_F16 what passes
+ *   65504 becomes infinite): the products' time of a plain layer.  dbias sums
+ *   its fp32 values either way.
  *   rows = 0 leaves zeros in dweight and dbias. */
 MPQ_API int64_t mpq_linear_backward_workspace_bytes(const void* dy, int64_t ldy, const void* x, int64_t ldx,
                                                     const void* weight, int64_t ldw, int64_t rows, int64_t n,

@@ -293,6 +293,16 @@ __host__ __device__ constexpr uint32_t lin_idesc(int M, int N) {
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// The contraction of a product: `steps` of BK in all.  An operand in two parts
+// (dz of a smooth activation: what 16 bits hold, and what they leave) takes
+// two steps per BK, first part first, so that the other operand's second copy
+// comes from L2.
+struct Contraction {
+  int steps, two;
+  __device__ __forceinline__ int at(int i) const { return (i >> two) * BK; }
+  __device__ __forceinline__ bool second(int i) const { return (i & two) != 0; }
+};
+
 struct LinOut {
   const void* bias;      // n values in T or fp32, or NULL
   const void* residual;  // rows x n in the output's type, or NULL
@@ -384,8 +394,9 @@ __device__ __forceinline__ void walk_tile(const Walk& w, int t, int& m0, int& n0
 // as a box may be, a commit reaches both CTAs, and descriptors are added up.
 template <typename T, typename O, bool A_MN, bool B_MN, bool FEAT>
 __global__ void __launch_bounds__(P_THREADS, 1)
-    k_lin_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-               const __grid_constant__ CUtensorMap tb_half, int KC, const __grid_constant__ LinOut o) {
+    k_lin_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap ta_second,
+               const __grid_constant__ CUtensorMap tb, const __grid_constant__ CUtensorMap tb_half,
+               const __grid_constant__ Contraction kc, const __grid_constant__ LinOut o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* stg_all = smem + P_RING;
@@ -400,7 +411,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   const int worker = (int)cluster_id_x(), nworkers = (int)(gridDim.x / 2);
   constexpr int CHAIN = chain_steps<O>();
   const Walk walk = make_walk(o.rows, o.cols, nworkers);
-  const int KT = (KC + BK - 1) / BK;
+  const int KT = kc.steps;
   const int stages = walk.whole ? 6 : 8, stage = walk.whole ? P_RING / 6 : P_RING / 8;
 
   if (threadIdx.x == 0) {
@@ -447,7 +458,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       const int r0 = is_a ? m0 + (int)rank * 128 : n0 + (int)rank * (wn / 2);
       const uint32_t bytes = (uint32_t)((128 + wn / 2) * BK * 2);
       const CUtensorMap* tm = wn == PT ? &tb : &tb_half;
-      for (int k0 = 0; k0 < KT * BK; k0 += BK, ++it) {
+      for (int i = 0; i < KT; ++i, ++it) {
+        const int k0 = kc.at(i);
         if (!mbar_wait(&empty[s], phase)) {
           atomicOr(&g_lin_status, STATUS_TIMEOUT);
           ok = false;
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         uint8_t* dst = dst0 + s * stage;
         if (is_a) {
           if (rank == 0) mbar_expect_tx(&full[s], 2 * bytes);
-          load_tile<A_MN, true>(&ta, fb, dst, r0, k0, 128);
+          load_tile<A_MN, true>(kc.second(i) ? &ta_second : &ta, fb, dst, r0, k0, 128);
         } else {
           load_tile<B_MN, true>(tm, fb, dst, r0, k0, wn / 2);
         }
@@ -734,6 +746,7 @@ __host__ __device__ inline int split_recv_bytes(int NT, int S) { return S > 1 ? 
 template <typename T, typename O, bool A_MN, bool B_MN, bool CHAINS, int NC>
 __global__ void __launch_bounds__(S_THREADS, NC == 1 || !CHAINS ? 2 : 1)
     k_lin_split(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                const __grid_constant__ CUtensorMap tb_second, const __grid_constant__ Contraction kc,
                 const __grid_constant__ SplitGeom g, const __grid_constant__ LinOut o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -793,11 +806,11 @@ __global__ void __launch_bounds__(S_THREADS, NC == 1 || !CHAINS ? 2 : 1)
         break;
       }
       uint8_t* a = smem + s * stage;
-      const int k0 = (k_lo + i) * BK;
+      const int k0 = kc.at(k_lo + i);
       const uint32_t fb = smem_u32(&full[s]);
       mbar_expect_tx(&full[s], (uint32_t)stage);
       load_tile<A_MN, false>(&ta, fb, a, a0, k0, 128);
-      load_tile<B_MN, false>(&tb, fb, a + 128 * BK * 2, b0, k0, g.NT);
+      load_tile<B_MN, false>(kc.second(k_lo + i) ? &tb_second : &tb, fb, a + 128 * BK * 2, b0, k0, g.NT);
       if (++s == g.stages) {
         s = 0;
         phase ^= 1;
@@ -1064,15 +1077,28 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// dz = dy * act'(z), rounded to the operands' type for the tensor cores (half
-// a step of that type per element, which the products' sums average; dbias
-// sums the unrounded values), and per block of 64 rows the column sums.
+// x as two values of 16 bits, for the tensor cores: x rounded, and what that
+// leaves, rounded.  Together within 2^-16 of x in bf16 and 2^-22 in fp16 (and
+// 2^-25 absolute).  What a first part of 16 bits cannot hold, the second does
+// (fp16: up to 131008).
+template <typename T>
+__device__ __forceinline__ void two_parts(float x, float& first, float& second) {
+  constexpr float top = std::is_same<T, __half>::value ? 65504.0f : 3.3895313892515355e38f;
+  first = to_f(from_f<T>(x));
+  if (isinf(first) && !isinf(x)) first = copysignf(top, x);
+  second = isfinite(first) ? x - first : 0.0f;
+}
+// dz = dy * act'(z) as the tensor cores take it, and per block of 64 rows the
+// column sums of its fp32 values.  The slopes of relu are 0 and 1, so its dz has
+// dy's type as it is; that of the smooth activations comes in two parts
+// (dz_second), or rounded to one (half a step of the type per element) where the
+// caller asked for that.
 constexpr int DZ_ROWS = 64;
 template <typename T>
 __global__ void __launch_bounds__(256, 3)
     k_lin_dz(const T* __restrict__ dy, int64_t ldy, const T* __restrict__ z, int64_t ldz, int act,
-             int64_t rows, int64_t n, T* __restrict__ dz, int64_t ldd, float* __restrict__ part,
-             bool vec_y, bool vec_z) {
+             int64_t rows, int64_t n, T* __restrict__ dz, T* __restrict__ dz_second, int64_t ldd,
+             float* __restrict__ part, bool vec_y, bool vec_z) {
   __shared__ float red[8][256 + 8];
   const int cg = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.y * 256 + cg * 8;
@@ -1099,6 +1125,12 @@ __global__ void __launch_bounds__(256, 3)
         if (dz) {  // ldd is a multiple of 8: the pad is zero
           float v[8];
           unpairs(g, v);
+          if (dz_second) {
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) two_parts<T>(v[j], v[j], w[j]);
+            store_vec<8>(dz_second + r * ldd + c, w, true);
+          }
           store_vec<8>(dz + r * ldd + c, v, true);
         }
 #pragma unroll
@@ -1166,10 +1198,12 @@ mpq_status encode_box(CUtensorMap* tm, const void* base, int64_t inner, int64_t 
   return MPQ_OK;
 }
 
-// An operand in memory: `rows` rows of `inner` contiguous elements.
+// An operand in memory: `rows` rows of `inner` contiguous elements; `second`:
+// its second part, laid out alike, or NULL.
 struct Operand {
   const void* p;
   int64_t inner, rows, ld;
+  const void* second = nullptr;
 };
 bool tma_ok(const void* p, int64_t inner, int64_t rows, int64_t ld) {
   return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (ld % 8 == 0 && ld >= inner));
@@ -1326,15 +1360,17 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
   int dev = 0, sms = 0;
   MPQ_TRY(lin_device(&dev, &sms));
   constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-  const int64_t KT = cdiv(KC, BK);
+  const Contraction kc{(int)cdiv(KC, BK) * (R.second ? 2 : 1), R.second ? 1 : 0};
+  const int64_t KT = kc.steps;
   const int64_t big = cdiv(o.rows, PT) * cdiv(o.cols, PT);
   const int pairs = g_lin_dev[dev].pairs;
   const SplitGeom g = split_geom(o, RN, KT, sms, chain_steps<O>());
   const int64_t at_ = cdiv(o.cols, 128), bt = cdiv(o.rows, g.NT);
   ProfScope ps_(tag, st);
   if (pairs > 0 && o.rows > 128 && (bt > 65535 || pair_us(o, KT, pairs) <= split_us(at_ * bt, g, sms))) {
-    CUtensorMap ta, tb, tb_half;
+    CUtensorMap ta, ta_second, tb, tb_half;
     MPQ_TRY(encode_box(&ta, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : 128));
+    MPQ_TRY(encode_box(&ta_second, R.second ? R.second : R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : 128));
     MPQ_TRY(encode_box(&tb, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
     MPQ_TRY(encode_box(&tb_half, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, 64));
     cudaLaunchConfig_t cfg = {};
@@ -1352,13 +1388,14 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
     auto kern = k_lin_pair<T, O, RN, CN, false>;
     if constexpr (!RN && !CN)
       if (o.act != MPQ_ACT_NONE || o.residual || o.preact) kern = k_lin_pair<T, O, RN, CN, true>;
-    MPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, ta, tb, tb_half, (int)KC, o));
+    MPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, ta, ta_second, tb, tb_half, kc, o));
   } else {
     if (bt > 65535 || at_ > 65535) return fail(MPQ_ERR_INVALID_ARG, "linear: too many tiles");
     const int smem = g.stages * split_stage_bytes(g.NT) + split_recv_bytes(g.NT, g.S) + (2 * g.stages + 6) * 8 + 16 + 1024;
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, tb_second;
     MPQ_TRY(encode_box(&ta, Cc.p, Cc.inner, Cc.rows, tma_ld(Cc), bf, CN ? 64 : 128));
     MPQ_TRY(encode_box(&tb, R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : g.NT));
+    MPQ_TRY(encode_box(&tb_second, R.second ? R.second : R.p, R.inner, R.rows, tma_ld(R), bf, RN ? 64 : g.NT));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)g.S, (unsigned)at_, (unsigned)bt);
     cfg.blockDim = dim3(S_THREADS);
@@ -1371,7 +1408,7 @@ mpq_status lin_product(const Operand& R, const Operand& Cc, int64_t KC, const Li
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    MPQ_CUDA(cudaLaunchKernelEx(&cfg, split_kernel<T, O, RN, CN>(g.chains, g.NT), ta, tb, g, o));
+    MPQ_CUDA(cudaLaunchKernelEx(&cfg, split_kernel<T, O, RN, CN>(g.chains, g.NT), ta, tb, tb_second, kc, g, o));
   }
   count_launch();
   return check_launch(tag);
@@ -1423,19 +1460,22 @@ mpq_status linear_fwd(Operand x, Operand w, const LinOut& o, char* ws, cudaStrea
 }
 
 struct BackPlan {  // workspace of a backward pass, in order
-  bool make_dz, pack_x, pack_w, sums;
-  int64_t dz, x, w, part, total;
+  bool make_dz, two_parts, pack_x, pack_w, sums;
+  int64_t dz, dz_second, x, w, part, total;
 };
 BackPlan back_plan(const void* dy, int64_t ldy, const void* x, int64_t ldx, const void* w, int64_t ldw,
-                   int64_t rows, int64_t n, int64_t k, int32_t act, bool need_dx, bool need_dw, bool need_db) {
+                   int64_t rows, int64_t n, int64_t k, int32_t act_flags, bool need_dx, bool need_dw, bool need_db) {
   BackPlan p{};
+  const int32_t act = act_flags & ~MPQ_DZ_ROUNDED;
   const bool prod = need_dx || need_dw;
   p.make_dz = prod && (act != MPQ_ACT_NONE || !tma_ok(dy, n, rows, ldy));
+  p.two_parts = prod && act > MPQ_ACT_RELU && !(act_flags & MPQ_DZ_ROUNDED);
   p.pack_x = need_dw && !tma_ok(x, k, rows, ldx);
   p.pack_w = need_dx && !tma_ok(w, k, n, ldw);
   p.sums = need_db;
   p.dz = 0;
-  p.x = p.dz + (p.make_dz ? packed_bytes(n, rows) : 0);
+  p.dz_second = p.dz + rows * round_up(n, 8) * 2;
+  p.x = p.dz + (p.make_dz ? packed_bytes(n, rows * (p.two_parts ? 2 : 1)) : 0);
   p.w = p.x + (p.pack_x ? packed_bytes(k, rows) : 0);
   p.part = p.w + (p.pack_w ? packed_bytes(k, n) : 0);
   p.total = p.part + (p.sums ? round_up(cdiv(rows, DZ_ROWS) * n * 4, 256) : 0);
@@ -1449,12 +1489,13 @@ mpq_status linear_bwd(const void* dy, int64_t ldy, Operand x, Operand w, const v
   Operand dz{dy, n, rows, ldy};
   if (p.make_dz || p.sums) {
     T* dzp = p.make_dz ? reinterpret_cast<T*>(ws + p.dz) : nullptr;
+    T* dz2 = p.two_parts ? reinterpret_cast<T*>(ws + p.dz_second) : nullptr;
     float* part = p.sums ? reinterpret_cast<float*>(ws + p.part) : nullptr;
     const int64_t ldd = round_up(n, 8), blocks = cdiv(rows, DZ_ROWS);
     {
       ProfScope ps_("k_lin_dz", st);
       k_lin_dz<T><<<dim3((unsigned)blocks, (unsigned)cdiv(n, 256)), 256, 0, st>>>(
-          static_cast<const T*>(dy), ldy, static_cast<const T*>(z), ldz, act, rows, n, dzp, ldd, part,
+          static_cast<const T*>(dy), ldy, static_cast<const T*>(z), ldz, act, rows, n, dzp, dz2, ldd, part,
           aligned_rows(dy, ldy, 2, 16), aligned_rows(z, ldz, 2, 16));
     }
     count_launch();
@@ -1468,7 +1509,7 @@ mpq_status linear_bwd(const void* dy, int64_t ldy, Operand x, Operand w, const v
       count_launch();
       MPQ_TRY(check_launch("k_lin_colsum"));
     }
-    if (p.make_dz) dz = Operand{dzp, n, rows, ldd};
+    if (p.make_dz) dz = Operand{dzp, n, rows, ldd, dz2};
   }
   MPQ_TRY(pack(&x, p.pack_x ? ws + p.x : nullptr, &w, p.pack_w ? ws + p.w : nullptr, st));
   LinOut o{};
@@ -1556,6 +1597,8 @@ extern "C" mpq_status mpq_linear_backward(const void* dy, int64_t ldy, const voi
                                           int64_t rows, int64_t n, int64_t k, int32_t dtype, int32_t act,
                                           void* dx, void* dweight, void* dbias, int32_t dbias_dtype,
                                           void* workspace, int64_t workspace_bytes, mpq_stream_t stream) {
+  const int32_t act_flags = act;
+  act &= ~MPQ_DZ_ROUNDED;
   MPQ_TRY(check_dims("linear_backward", rows, n, k, dtype, act));
   if (dbias && dbias_dtype != dtype && dbias_dtype != MPQ_F32)
     return fail(MPQ_ERR_INVALID_ARG, "linear_backward: dbias must have the operands' type or fp32");
@@ -1567,7 +1610,7 @@ extern "C" mpq_status mpq_linear_backward(const void* dy, int64_t ldy, const voi
   }
   if (!dy || (dweight && !x) || (dx && !weight) || (act != MPQ_ACT_NONE && !preact))
     return fail(MPQ_ERR_INVALID_ARG, "linear_backward: missing buffer");
-  const BackPlan p = back_plan(dy, ldy, x, ldx, weight, ldw, rows, n, k, act, dx != nullptr, dweight != nullptr,
+  const BackPlan p = back_plan(dy, ldy, x, ldx, weight, ldw, rows, n, k, act_flags, dx != nullptr, dweight != nullptr,
                                dbias != nullptr);
   if (p.total > 0 && (!workspace || workspace_bytes < p.total || ((uintptr_t)workspace & 255)))
     return fail(MPQ_ERR_INVALID_ARG, "linear_backward: needs " + std::to_string(p.total) +
