@@ -488,11 +488,12 @@ MPQ_API mpq_status mpq_layer_norm_backward(const void* dy, int64_t ldy, const vo
  *   logits: rows x v of `dtype`.  tokens: rows int64, or NULL (then logprob
  *   must be NULL).  0 <= top <= min(v, MPQ_TOP_MAX); top_logprob, top_id: rows
  *   x top, NULL for top = 0.  entropy may be NULL.
- *   Logits of -inf and of the type's lowest value have probability 0.  A row
- *   whose logits are all -inf has no distribution: logprob and top_logprob
- *   are -inf, entropy 0.  A row with a NaN or +inf (or a logit above 2^127)
- *   gives NaN, and top_id ranks its logits that are no NaN (-1 where there
- *   are too few).
+ *   Any finite logit is one, a mask's -1e10 or the type's lowest value too: next
+ *   to ordinary ones it has probability 0, and a row of nothing else is uniform.
+ *   -inf has probability 0.  A row whose logits are all -inf has no
+ *   distribution: logprob and top_logprob are -inf, entropy 0.  A row with a NaN
+ *   or +inf gives NaN, and top_id ranks its logits that are no NaN (-1 where
+ *   there are too few).
  *   0 <= rows <= 2^24, 1 <= v <= 2^24. */
 #define MPQ_TOP_MAX 128
 MPQ_API mpq_status mpq_token_logprobs(const void* logits, int64_t ldl, int64_t rows, int64_t v, int32_t dtype,
@@ -512,6 +513,8 @@ MPQ_API mpq_status mpq_token_logprobs(const void* logits, int64_t ldl, int64_t r
  *   twice adds both entries.  0.001 <= T <= 1000.  A row with no entry left, and every row of
  *   weight 0, has gradient 0; the first also loss 0.  An id >= v makes its
  *   row's loss and gradient NaN.
+ *   Finite logits may have any size, as for mpq_token_logprobs.  A student's row
+ *   of nothing but -inf has p = 0: loss +inf where the teacher has an entry.
  *   0 <= rows <= 2^24, 1 <= v <= 2^24. */
 MPQ_API mpq_status mpq_topk_distill(const void* logits, int64_t ldl, int64_t rows, int64_t v, int32_t dtype,
                                     const float* top_logits, const int64_t* top_ids, int32_t top,

@@ -3,11 +3,12 @@
 // teacher's top logits and the student's gradient).
 //
 // One pass over a row of v logits with the running maximum and sums of a
-// softmax, in powers of two: with k = log2(e) / T and M the row's maximum of
-// l k, S = sum 2^(l k - M) and U = sum (l k - M) 2^(l k - M), so that
-//   log p_t = ln2 (l_t k - M) - ln S,   H = ln S - ln2 U / S.
-// fma(l, k, -M) rounds once, with the same rounded M everywhere, so M's own
-// rounding cancels.  A cluster of C CTAs shares a row when there are few rows
+// softmax, in powers of two: with k = log2(e) / T, M the row's largest logit and
+// y = (l - M) k, S = sum 2^y and U = sum y 2^y, so that
+//   log p_t = (l_t - M) / T - ln S,   H = ln S - ln2 U / S.
+// The maximum is subtracted before the scaling, so that its own y is 0 whatever
+// its size: in l k - M k a rounded M k leaves half a step of M k, which for a
+// finite mask of -1e10 is hundreds.  A cluster of C CTAs shares a row when there are few rows
 // (each takes a stretch of the columns; sums and top lists meet over
 // distributed shared memory in rank order).
 //
@@ -21,8 +22,8 @@
 //
 // What bounds them: HBM by the bytes, and before it the issue of an exponential
 // and its arithmetic per element.  At 1024 rows of 131072 bf16 logits (268 MB):
-// token_logprobs without alternatives 58 us (4.6 TB/s), with 20 alternatives 77
-// (3.5 TB/s; 61% of the issue slots); topk_distill, which reads the row twice
+// token_logprobs without alternatives 60 us (4.5 TB/s), with 20 alternatives 78
+// (3.4 TB/s; 61% of the issue slots); topk_distill, which reads the row twice
 // and writes the gradient, 125 us against 82 for the bytes read once.
 #include <algorithm>
 #include <type_traits>
@@ -35,7 +36,8 @@ namespace {
 constexpr int TOP_SETS = 128;      // sets of columns whose maxima bound the top list
 constexpr int CAND = 4096;         // candidates ranked at once
 constexpr int64_t L2_ROWS = 96ll << 20;  // logits at work that L2 (126 MB) is trusted with
-constexpr float M_FLOOR = -1e37f;  // start of the running maximum (scaled)
+constexpr float M_FLOOR = -3.4028234663852886e38f;  // start of the running maximum: fp32's lowest value
+constexpr float Y_FLOOR = -150.0f;  // an exponent whose power is 0, and stays finite times a sum
 constexpr float LN2 = 0.69314718055994531f, LOG2E = 1.4426950408889634f;
 static_assert(TOP_SETS >= MPQ_TOP_MAX, "a bound needs `top` sets");
 
@@ -87,13 +89,14 @@ __device__ __forceinline__ Raw8<T> encode(const float (&x)[8]) {
   return r;
 }
 
-struct Soft {  // the running softmax: scaled maximum, sums
+struct Soft {  // the running softmax: maximum, sums
   float m, s, u;
 };
 template <bool ENT>
-__device__ __forceinline__ Soft merge(const Soft& a, const Soft& b) {
+__device__ __forceinline__ Soft merge(const Soft& a, const Soft& b, float k) {
   const float m = fmaxf(a.m, b.m);
-  const float da = a.m - m, db = b.m - m;
+  // (a maximum of +inf has a NaN for its sum already)
+  const float da = fmaxf((a.m - m) * k, Y_FLOOR), db = fmaxf((b.m - m) * k, Y_FLOOR);
   const float ca = ex2(da), cb = ex2(db);
   Soft r;
   r.m = m;
@@ -102,14 +105,14 @@ __device__ __forceinline__ Soft merge(const Soft& a, const Soft& b) {
   return r;
 }
 template <bool ENT>
-__device__ __forceinline__ Soft warp_merge(Soft a) {
+__device__ __forceinline__ Soft warp_merge(Soft a, float k) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     Soft b;
     b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
     b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
     b.u = ENT ? __shfl_xor_sync(0xffffffffu, a.u, o) : 0.0f;
-    a = merge<ENT>(a, b);
+    a = merge<ENT>(a, b, k);
   }
   return a;
 }
@@ -152,22 +155,22 @@ __device__ __forceinline__ Soft scan_row(const Row<T>& row, int lo, int hi, floa
         best_g = g0 + j * AT;
       }
       const float old = m;
-      m = fmaxf(m, top * k);
-      const float d = old - m, c = ex2(d);
+      m = fmaxf(m, top);
+      const float d = fmaxf((old - m) * k, Y_FLOOR), c = ex2(d);
       const uint64_t c2 = f2_pack(c, c);
       if (ENT) u2 = f2_mul(c2, f2_fma(f2_pack(d, d), s2, u2));
       s2 = f2_mul(s2, c2);
       const uint64_t m2 = f2_pack(-m, -m);
       float y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), k2, m2), y[2 * i], y[2 * i + 1]);
+      for (int i = 0; i < 4; ++i)
+        f2_unpack(f2_mul(f2_add(f2_pack(x[2 * i], x[2 * i + 1]), m2), k2), y[2 * i], y[2 * i + 1]);
       if (ENT) {
-        // masked logits: 2^-150 is 0 here, and keeps 0 * (-inf) out of the
-        // entropy's sum
+        // masked logits: keeps 0 * (-inf) out of the entropy's sum
         const float low = fmin3(fmin3(fmin3(y[0], y[1], y[2]), y[3], y[4]), fminf(y[5], y[6]), y[7]);
-        if (low < -150.0f) {
+        if (low < Y_FLOOR) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = max_nan(y[i], -150.0f);
+          for (int i = 0; i < 8; ++i) y[i] = max_nan(y[i], Y_FLOOR);
         }
       }
 #pragma unroll
@@ -189,18 +192,14 @@ __device__ __forceinline__ Soft scan_row(const Row<T>& row, int lo, int hi, floa
 
 struct RowStat {
   Soft a;
-  float raw;    // the largest logit (set when `flat`)
   float logs;   // ln S
-  bool flat;    // every logit is below M_FLOOR: only those equal to the largest count
-  bool empty;   // all are -inf
+  bool empty;   // all logits are -inf: S = 0 (else the largest adds 1)
 };
 
 template <int AT>
 struct AnsShared {
   Soft warp[AT / 32];
   Soft cta;               // this CTA's part of the row (read by the cluster)
-  float cta_raw, warp_raw[AT / 32];
-  float cta_count, warp_count[AT / 32];
 };
 
 template <bool CL>
@@ -219,19 +218,17 @@ __device__ __forceinline__ uint64_t ld_cluster64(const uint64_t* p, int rank) {
 }
 
 // Joins the threads' softmaxes over the CTA and the cluster of C CTAs; every
-// thread gets the row's.  Rows whose logits all lie below the floor are
-// counted here: the spacing of fp32 there is so wide that a logit either
-// equals the largest or has probability 0.
-template <int AT, typename T, bool ENT, bool CL>
-__device__ __forceinline__ RowStat join_row(const Row<T>& row, int lo, int hi, Soft a, int C, AnsShared<AT>& sh) {
+// thread gets the row's.
+template <int AT, bool ENT, bool CL>
+__device__ __forceinline__ RowStat join_row(Soft a, float k, int C, AnsShared<AT>& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  a = warp_merge<ENT>(a);
+  a = warp_merge<ENT>(a, k);
   if (lane == 0) sh.warp[warp] = a;
   __syncthreads();
   if (warp == 0) {
     Soft b{M_FLOOR, 0.0f, 0.0f};
     if (lane < AT / 32) b = sh.warp[lane];
-    b = warp_merge<ENT>(b);
+    b = warp_merge<ENT>(b, k);
     if (lane == 0) sh.cta = b;
   }
   sync_row<CL>();
@@ -243,67 +240,22 @@ __device__ __forceinline__ RowStat join_row(const Row<T>& row, int lo, int hi, S
       b.s = ld_cluster(&sh.cta.s, lane);
       b.u = ENT ? ld_cluster(&sh.cta.u, lane) : 0.0f;
     }
-    st.a = warp_merge<ENT>(b);
+    st.a = warp_merge<ENT>(b, k);
   } else {
     st.a = sh.cta;
   }
-  st.flat = st.a.m <= M_FLOOR && st.a.s == 0.0f;  // (a NaN makes s NaN: not flat)
-  st.empty = false;
-  st.raw = 0.0f;
-  if (st.flat) {  // the same in all threads of the cluster
-    float mx = -INFINITY;
-    for (int g = lo + (int)threadIdx.x; g < hi; g += AT) {
-      float x[8];
-      decode<T>(row.load(g), x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, x[i]);
-    }
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) sh.warp_raw[warp] = mx;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < AT / 32; ++w) mx = fmaxf(mx, sh.warp_raw[w]);
-      sh.cta_raw = mx;
-    }
-    sync_row<CL>();
-    mx = sh.cta_raw;
-    if (CL)
-      for (int r = 0; r < C; ++r) mx = fmaxf(mx, ld_cluster(&sh.cta_raw, r));
-    float cnt = 0.0f;
-    if (mx > -INFINITY)
-      for (int g = lo + (int)threadIdx.x; g < hi; g += AT) {
-        float x[8];
-        decode<T>(row.load(g), x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cnt += x[i] == mx ? 1.0f : 0.0f;
-      }
-    for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-    if (lane == 0) sh.warp_count[warp] = cnt;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < AT / 32; ++w) cnt += sh.warp_count[w];
-      sh.cta_count = cnt;
-    }
-    sync_row<CL>();
-    cnt = CL ? 0.0f : sh.cta_count;
-    if (CL)
-      for (int r = 0; r < C; ++r) cnt += ld_cluster(&sh.cta_count, r);
-    st.raw = mx;
-    st.empty = !(mx > -INFINITY);
-    st.a.s = cnt;
-    st.a.u = 0.0f;
-  }
+  st.empty = st.a.s == 0.0f;
   st.logs = st.empty ? 0.0f : logf(st.a.s);
   return st;
 }
 
 // log p of a logit x of the row
-__device__ __forceinline__ float log_prob(const RowStat& st, float x, float k, float inv_t) {
+__device__ __forceinline__ float log_prob(const RowStat& st, float x, float inv_t) {
   if (st.empty) return -INFINITY;
-  if (st.flat) return (x - st.raw) * inv_t - st.logs;
-  const float y = fmaf(x, k, -st.a.m);
-  if (y > -INFINITY || x == -INFINITY || y != y) return fmaf(y, LN2, -st.logs);
-  return x * inv_t - fmaf(st.a.m, LN2, st.logs);  // a finite logit whose scaled value overflows
+  const float d = x - st.a.m;
+  if (d == -INFINITY && x > -INFINITY)  // their distance overflows, which a temperature may bring back
+    return fmaf(x, inv_t, -fmaf(st.a.m, inv_t, st.logs));
+  return fmaf(d, inv_t, -st.logs);
 }
 
 // ---------------------------------------------------------- token_logprobs --
@@ -484,12 +436,12 @@ __global__ void __launch_bounds__(AT, 1024 / AT) k_token_logprobs(const __grid_c
   int best_g;
   const Soft part = scan_row<AT, T, true, TOP>(row, lo, hi, LOG2E, best, best_g);
   if constexpr (TOP) cta_top<AT, T>(row, lo, hi, a.top, best, best_g, part.s != part.s, top_sh);
-  const RowStat st = join_row<AT, T, true, CL>(row, lo, hi, part, a.C, sh);  // (its barriers publish the top lists)
+  const RowStat st = join_row<AT, true, CL>(part, LOG2E, a.C, sh);  // (its barriers publish the top lists)
   if (rank == 0 && threadIdx.x == 0) {
     if (a.logprob) {
       const int64_t t = a.tokens[r];
       float lp = 0.0f;
-      if (t != a.ignore) lp = (t < 0 || t >= a.v) ? NAN : log_prob(st, to_f(row.p[t]), LOG2E, 1.0f);
+      if (t != a.ignore) lp = (t < 0 || t >= a.v) ? NAN : log_prob(st, to_f(row.p[t]), 1.0f);
       a.logprob[r] = lp;
     }
     if (a.entropy) a.entropy[r] = st.empty ? 0.0f : max_nan(0.0f, fmaf(-LN2, st.a.u / st.a.s, st.logs));
@@ -498,7 +450,7 @@ __global__ void __launch_bounds__(AT, 1024 / AT) k_token_logprobs(const __grid_c
     auto put = [&](int at, uint64_t key) {
       const int64_t o = r * a.top + at;
       a.top_id[o] = key ? (int64_t)(0xffffffffu - (uint32_t)key) : -1;
-      a.top_logprob[o] = (key || st.a.s != st.a.s) ? log_prob(st, key_value((uint32_t)(key >> 32)), LOG2E, 1.0f) : -INFINITY;
+      a.top_logprob[o] = (key || st.a.s != st.a.s) ? log_prob(st, key_value((uint32_t)(key >> 32)), 1.0f) : -INFINITY;
     };
     if (!CL) {
       if ((int)threadIdx.x < a.top) put((int)threadIdx.x, top_sh.list[threadIdx.x]);
@@ -590,13 +542,13 @@ __global__ void __launch_bounds__(AT, 1024 / AT) k_topk_distill(const __grid_con
   float best;
   int best_g;
   const Soft part = scan_row<AT, T, false, false>(row, lo, hi, a.k, best, best_g);
-  const RowStat st = join_row<AT, T, false, CL>(row, lo, hi, part, a.C, sh);
+  const RowStat st = join_row<AT, false, CL>(part, a.k, a.C, sh);
   if (rank == 0 && threadIdx.x < 32) {
     float l = 0.0f;
     for (int e = threadIdx.x; e < a.top; e += 32) {
       const float q = te.q[e];
       if (te.id[e] >= 0 && q != 0.0f)  // (a NaN entry counts)
-        l = fmaf(q, te.logq[e] - log_prob(st, to_f(row.p[te.id[e]]), a.k, a.inv_t), l);
+        l = fmaf(q, te.logq[e] - log_prob(st, to_f(row.p[te.id[e]]), a.inv_t), l);
     }
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (threadIdx.x == 0) a.loss[r] = te.bad ? NAN : te.live ? l : 0.0f;
@@ -625,10 +577,6 @@ __global__ void __launch_bounds__(AT, 1024 / AT) k_topk_distill(const __grid_con
       memcpy(&r, e, sizeof(r));
       return r;
     };
-    auto prob = [&](float x) {  // p times its row's sum
-      if (st.flat) return (!st.empty && x == st.raw) ? 1.0f : 0.0f;
-      return ex2(fmaf(x, a.k, -st.a.m));
-    };
     constexpr int U = sizeof(T) == 4 ? 2 : 4;
     const uint64_t k2 = f2_pack(a.k, a.k), m2 = f2_pack(-st.a.m, -st.a.m), c2 = f2_pack(cs, cs);
     // from the end of the row, which L2 got last (132 us become 128 at 1024 rows
@@ -645,14 +593,14 @@ __global__ void __launch_bounds__(AT, 1024 / AT) k_topk_distill(const __grid_con
         if (g >= hi2) break;
         float x[8];
         decode<T>(raw[j], x);
-        if (st.flat || zero) {
+        if (zero) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = zero ? 0.0f : cs * prob(x[i]);
+          for (int i = 0; i < 8; ++i) x[i] = 0.0f;
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 4; ++i) {  // cs 2^y
             float y0, y1;
-            f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), k2, m2), y0, y1);
+            f2_unpack(f2_mul(f2_add(f2_pack(x[2 * i], x[2 * i + 1]), m2), k2), y0, y1);
             f2_unpack(f2_mul(f2_pack(ex2(y0), ex2(y1)), c2), x[2 * i], x[2 * i + 1]);
           }
         }
@@ -684,7 +632,7 @@ __global__ void __launch_bounds__(AT, 1024 / AT) k_topk_distill(const __grid_con
           q += te.q[j];
         }
       if (!first) continue;
-      const float p = st.empty ? 0.0f : prob(to_f(row.p[id])) / st.a.s;
+      const float p = st.empty ? 0.0f : ex2((to_f(row.p[id]) - st.a.m) * a.k) / st.a.s;
       out[id] = from_f<T>(c * (p - q));
     }
   }
