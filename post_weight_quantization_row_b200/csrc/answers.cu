@@ -343,7 +343,10 @@ __device__ __forceinline__ void cta_top(const Row<T>& row, int lo, int hi, int t
   // keys of vectors: (largest logit, vector); every one of the top logits has
   // (logit, its vector) >= bound
   const uint64_t bound = sh.bound;
-  if (mine != 0 && mine >= bound) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = tid;
+  // (a thread with the lowest key may hold logits of -inf next to its NaN: read
+  // where the bound is one)
+  const bool hidden = mine == 1 && bound <= full_key(-INFINITY, 0);
+  if (hidden || (mine != 0 && mine >= bound)) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = tid;
   __syncthreads();
   const int per = (hi - lo + AT - 1) / AT, items = sh.n_flagged * per;
   const float floor_x = bound > 1 ? key_value((uint32_t)(bound >> 32)) : -INFINITY;

@@ -126,3 +126,32 @@ def test_rows_of_large_logits(mpq, size, many):
                             temperature=1e3)["loss"]
     want = 2e-3 * float(torch.tensor(size)) + math.log((v + 1) // 2)  # log p of -size next to size, over T = 1000
     assert abs(float(lost) - want) <= 8 * U * want + 64 * U * math.log(v)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 300])
+@pytest.mark.parametrize("v,top", [(9, 9), (700, 20), (20000, 9), (20000, 128), (90000, 100)])
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+def test_top_ids_of_masked_rows_with_nan(mpq, rows, v, top, dtype):
+    """Of a row with a NaN the logits that are none are ranked, -inf among them (equal ones: lowest id first)."""
+    g = gen(v + rows)
+    l = torch.full((rows, v), -math.inf, device="cuda")
+    for r in range(rows):
+        kind = r % 4 if rows > 1 else 0
+        l[r, 5] = math.nan                                   # a NaN among the first columns
+        if kind == 1:                                        # and some all over, some finite logits
+            l[r, torch.randint(0, v, (v // 50 + 1,), generator=g, device="cuda")] = math.nan
+            l[r, torch.randint(0, v, (3,), generator=g, device="cuda")] = 1.5
+        elif kind == 2:                                      # whole threads' columns
+            l[r, : v // 3] = math.nan
+        elif kind == 3:                                      # fewer logits than are asked for
+            l[r] = math.nan
+            l[r, v - 2:] = -math.inf
+    l = l.to(dtype)
+    out = mpq.token_logprobs(l, top=top)
+    rank = torch.where(torch.isnan(l), torch.tensor(-1.0, device="cuda"), torch.where(l > -math.inf, 1.0, 0.0))
+    val, idx = torch.sort(rank, dim=-1, descending=True, stable=True)  # (finite ones are all 1.5)
+    want = torch.where(val[:, :top] < 0, -1, idx[:, :top])
+    assert torch.equal(out["top_id"], want)
+    # (among nine columns the finite logits may have taken the place of every NaN)
+    has = torch.isnan(l).any(-1)
+    assert torch.equal(torch.isnan(out["entropy"]), has) and torch.equal(torch.isnan(out["top_logprob"]).all(-1), has)
