@@ -155,3 +155,18 @@ def test_top_ids_of_masked_rows_with_nan(mpq, rows, v, top, dtype):
     # (among nine columns the finite logits may have taken the place of every NaN)
     has = torch.isnan(l).any(-1)
     assert torch.equal(torch.isnan(out["entropy"]), has) and torch.equal(torch.isnan(out["top_logprob"]).all(-1), has)
+
+
+# Vectors of 8 columns belong to threads in turn (256 of them here); 40 threads hold large logits only, more than the
+# candidate buffer's 4096.  They fill 20 of the 128 sets whose maxima bound the list, so that for more than 20
+# alternatives all of them are candidates.  One CTA a row (300 rows), clusters of 8 (one row); many ties in 16 bits.
+@pytest.mark.parametrize("rows,v,dtype", [(300, 80000, BF), (300, 80000, HF), (300, 40960, F32), (1, 8 * 8 * 256 * 20, BF),
+                                          (1, 8 * 8 * 256 * 20, F32), (2, 8 * 8 * 256 * 15 + 5, HF)])
+@pytest.mark.parametrize("top", [1, 64, 128])
+def test_top_with_more_candidates_than_their_buffer(mpq, rows, v, dtype, top):
+    assert v // (8 if rows < 9 else 1) // 8 // 256 * 8 * 40 > 4096
+    l = torch.randn(rows, v, generator=gen(rows + top), device="cuda")
+    cta = v // 8 if rows < 9 else v  # columns of a CTA
+    cols = torch.arange(v, device="cuda") % cta
+    l[:, ((cols // 8) % 256 >= 3) & ((cols // 8) % 256 < 43)] += 100
+    check_logprobs(mpq, l.to(dtype), torch.zeros(rows, dtype=torch.int64, device="cuda"), top)
