@@ -395,8 +395,9 @@ MPQ_API mpq_status mpq_stage_energy_noalloc(mpq_plan_t plan, const float* W, int
  * (perplexity is the paper's own measure).  These need no plan.  Beyond the
  * conventions at the head of this file:
  *  - Rows may be strided: `ld*` is the distance between rows in elements,
- *    columns are contiguous; inputs need no alignment.  Outputs are
- *    contiguous.  Outputs must not overlap inputs or each other.
+ *    columns are contiguous; inputs need no alignment beyond that of their
+ *    elements (a pointer off that is refused).  Outputs are contiguous and must
+ *    not overlap inputs or each other.
  *  - Work runs on the current device, which must own every buffer.  The calls
  *    can be captured into graphs; scratch is the caller's (`workspace`, on a
  *    256-byte boundary, size from the _workspace_bytes function for the same

@@ -722,7 +722,8 @@ extern "C" mpq_status mpq_token_logprobs(const void* logits, int64_t ldl, int64_
   if (rows == 0) return MPQ_OK;
   if (!logits || (top > 0 && (!top_logprob || !top_id)))
     return fail(MPQ_ERR_INVALID_ARG, "token_logprobs: missing buffer");
-  if ((uintptr_t)logits % dtype_size(dtype)) return fail(MPQ_ERR_INVALID_ARG, "token_logprobs: misaligned logits");
+  MPQ_TRY(check_elements("token_logprobs", {{logits, dtype_size(dtype)}, {tokens, 8}, {logprob, 4}, {entropy, 4},
+                                            {top_logprob, 4}, {top_id, 8}}));
   int dev = 0, sms = 0;
   MPQ_TRY(current_device(&dev, &sms));
   LogprobArgs a{};
@@ -755,7 +756,8 @@ extern "C" mpq_status mpq_topk_distill(const void* logits, int64_t ldl, int64_t 
     return fail(MPQ_ERR_INVALID_ARG, "topk_distill: temperature must be in [1e-3, 1e3]");
   if (rows == 0) return MPQ_OK;
   if (!logits || !top_logits || !top_ids || !loss) return fail(MPQ_ERR_INVALID_ARG, "topk_distill: missing buffer");
-  if ((uintptr_t)logits % dtype_size(dtype)) return fail(MPQ_ERR_INVALID_ARG, "topk_distill: misaligned logits");
+  MPQ_TRY(check_elements("topk_distill", {{logits, dtype_size(dtype)}, {top_logits, 4}, {top_ids, 8}, {weight, 4},
+                                          {loss, 4}, {dlogits, dtype_size(dtype)}}));
   int dev = 0, sms = 0;
   MPQ_TRY(current_device(&dev, &sms));
   DistillArgs a{};

@@ -749,7 +749,8 @@ extern "C" mpq_status mpq_layer_norm(const void* x, int64_t ldx, int64_t rows, i
     return fail(MPQ_ERR_INVALID_ARG, "layer_norm: eps must be > 0");
   if (rows == 0) return MPQ_OK;
   if (!x || !y) return fail(MPQ_ERR_INVALID_ARG, "layer_norm: missing buffer");
-  const int64_t es = dtype_size(dtype);
+  const int64_t es = dtype_size(dtype), ps = dtype_size(param_dtype);
+  MPQ_TRY(check_elements("layer_norm", {{x, es}, {y, es}, {weight, ps}, {bias, ps}, {mean, 4}, {rstd, 4}}));
   LnArgs a{};
   a.x = x;
   a.ldx = ldx;
@@ -780,6 +781,9 @@ extern "C" mpq_status mpq_layer_norm_backward(const void* dy, int64_t ldy, const
                                               int64_t workspace_bytes, mpq_stream_t stream) {
   const bool sums = dweight || dbias;
   MPQ_TRY(ln_check("layer_norm_backward", rows, n, dtype, weight ? weight : dweight, dbias, param_dtype));
+  const int64_t es = dtype_size(dtype), ps = dtype_size(param_dtype);
+  MPQ_TRY(check_elements("layer_norm_backward", {{dy, es}, {x, es}, {mean, 4}, {rstd, 4}, {weight, ps}, {dx, es},
+                                                 {dweight, ps}, {dbias, ps}}));
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0) {
     const size_t bytes = (size_t)(n * dtype_size(param_dtype));
@@ -793,7 +797,6 @@ extern "C" mpq_status mpq_layer_norm_backward(const void* dy, int64_t ldy, const
   if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
     return fail(MPQ_ERR_INVALID_ARG, "layer_norm_backward: needs " + std::to_string(need) +
                                          " bytes of workspace on a 256-byte boundary");
-  const int64_t es = dtype_size(dtype);
   LnArgs a{};
   a.x = x;
   a.ldx = ldx;

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <initializer_list>
+
 #include "f32x2.cuh"
 #include "mpq_internal.cuh"
 #include "tc_ptx.cuh"
@@ -288,6 +290,19 @@ __device__ __forceinline__ float ld_cluster(const float* p, int rank) {
                : "r"(tcx::map_to_rank(tcx::smem_u32(p), (uint32_t)rank))
                : "memory");
   return v;
+}
+
+// Buffers that do not start on a multiple of their elements' size are refused:
+// a load or store of such an element is a fault on the device.
+struct Buffer {
+  const void* p;
+  int64_t elem;
+};
+inline mpq_status check_elements(const char* who, std::initializer_list<Buffer> buffers) {
+  for (const Buffer& b : buffers)
+    if ((uintptr_t)b.p % (uintptr_t)b.elem)
+      return fail(MPQ_ERR_INVALID_ARG, std::string(who) + ": a buffer is not aligned to its elements");
+  return MPQ_OK;
 }
 
 inline bool aligned_rows(const void* p, int64_t ld, int64_t elem, int64_t bytes) {

@@ -1554,6 +1554,8 @@ extern "C" mpq_status mpq_linear(const void* x, int64_t ldx, const void* weight,
     return fail(MPQ_ERR_INVALID_ARG, "linear: the bias must have the operands' type or fp32");
   if (rows == 0) return MPQ_OK;
   if (!x || !weight || !y) return fail(MPQ_ERR_INVALID_ARG, "linear: missing buffer");
+  MPQ_TRY(check_elements("linear", {{x, 2}, {weight, 2}, {bias, bias ? dtype_size(bias_dtype) : 1},
+                                    {residual, dtype_size(y_dtype)}, {preact, 2}, {y, dtype_size(y_dtype)}}));
   const int64_t need = mpq_linear_workspace_bytes(x, ldx, weight, ldw, rows, n, k);
   if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
     return fail(MPQ_ERR_INVALID_ARG, "linear: needs " + std::to_string(need) +
@@ -1602,6 +1604,8 @@ extern "C" mpq_status mpq_linear_backward(const void* dy, int64_t ldy, const voi
   MPQ_TRY(check_dims("linear_backward", rows, n, k, dtype, act));
   if (dbias && dbias_dtype != dtype && dbias_dtype != MPQ_F32)
     return fail(MPQ_ERR_INVALID_ARG, "linear_backward: dbias must have the operands' type or fp32");
+  MPQ_TRY(check_elements("linear_backward", {{dy, 2}, {x, 2}, {weight, 2}, {preact, 2}, {dx, 2}, {dweight, 2},
+                                             {dbias, dbias ? dtype_size(dbias_dtype) : 1}}));
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0) {  // nothing to sum: the parameters' gradients are zero
     if (dweight) MPQ_CUDA(cudaMemsetAsync(dweight, 0, (size_t)(n * k * 2), st));
