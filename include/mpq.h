@@ -522,10 +522,15 @@ MPQ_API mpq_status mpq_topk_distill(const void* logits, int64_t ldl, int64_t row
                                     const float* weight, double temperature, float* loss, void* dlogits,
                                     mpq_stream_t stream);
 
-/* Synchronise `stream`, read and clear the status of the layer operators on
- * the current device: MPQ_OK, or MPQ_ERR_TIMEOUT when a bounded wait of a
- * kernel ran out (its outputs are then undefined). */
+/* Synchronise `stream` and read the status of the layer operators on the
+ * current device: MPQ_OK, or MPQ_ERR_TIMEOUT when a bounded wait of a kernel, on
+ * whatever stream, ran out since this host thread's last call (its first: since
+ * the library was loaded); the outputs of the calls in between are then
+ * undefined.  Every thread gets to know of every timeout. */
 MPQ_API mpq_status mpq_ops_status(mpq_stream_t stream);
+/* For the tests of a caller's error handling: a kernel with a wait that runs
+ * out, in a microsecond, and is reported like any other's. */
+MPQ_API mpq_status mpq_ops_expire(mpq_stream_t stream);
 
 /* ----------------------------------------------------------- profiling --- */
 /* Per-kernel timing with CUDA events recorded on the launching stream around

@@ -103,6 +103,7 @@ _sig("mpq_layer_norm_backward", ST, P, I64, P, I64, P, P, I64, I64, I32, P, I32,
 _sig("mpq_token_logprobs", ST, P, I64, I64, I64, I32, P, I64, I32, P, P, P, P, P)
 _sig("mpq_topk_distill", ST, P, I64, I64, I64, I32, P, P, I32, P, F64, P, P, P)
 _sig("mpq_ops_status", ST, P)
+_sig("mpq_ops_expire", ST, P)
 _sig("mpq_profile_start", ST)
 _sig("mpq_profile_stop", ST, C.c_char_p, I64)
 _sig("mpq_last_error", C.c_char_p)
@@ -118,7 +119,7 @@ EXPORTED = ["mpq_params_default", "mpq_plan_create_from_spectrum", "mpq_plan_cre
             "mpq_stage_cd", "mpq_stage_energy", "mpq_stage_energy_noalloc",
             "mpq_linear_workspace_bytes", "mpq_linear", "mpq_linear_backward_workspace_bytes",
             "mpq_linear_backward", "mpq_layer_norm", "mpq_layer_norm_backward_workspace_bytes",
-            "mpq_layer_norm_backward", "mpq_token_logprobs", "mpq_topk_distill", "mpq_ops_status",
+            "mpq_layer_norm_backward", "mpq_token_logprobs", "mpq_topk_distill", "mpq_ops_status", "mpq_ops_expire",
             "mpq_profile_start", "mpq_profile_stop",
             "mpq_last_error", "mpq_kernel_launch_count"]
 

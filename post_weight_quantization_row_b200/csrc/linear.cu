@@ -47,8 +47,11 @@ namespace mpq {
 namespace {
 using namespace tcx;
 
-// Set by a wait that ran out (mpq_ops_status reads and clears it).
-__device__ int g_lin_status;
+// Counts the waits that ran out.  It only grows, and mpq_ops_status compares it
+// with what its thread saw last: nothing is cleared, so that no call takes a
+// timeout from another stream's or thread's.
+__device__ uint32_t g_timeouts;
+__device__ __forceinline__ void report_timeout() { atomicAdd(&g_timeouts, 1u); }
 
 // ------------------------------------------------------------ activations --
 // All from one 2^x and one reciprocal each (special function unit), in forms
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       for (int i = 0; i < KT; ++i, ++it) {
         const int k0 = kc.at(i);
         if (!mbar_wait(&empty[s], phase)) {
-          atomicOr(&g_lin_status, STATUS_TIMEOUT);
+          report_timeout();
           ok = false;
           break;
         }
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         }
       }
     }
-    if (!ok) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    if (!ok) report_timeout();
     for (uint32_t q = (tl > 2 ? tl - 2 : 0); q < tl; ++q)  // MMAs finish before TMEM is freed
       for (uint32_t i = 0; i < (1u << 25) && !mbar_try_wait(&tm_full[q & 1], (q / 2) & 1); ++i)
         if (i > 256) __nanosleep(64);
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         ++tl;
       }
       if (!ok) {
-        if (lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+        if (lane == 0) report_timeout();
         break;
       }
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)buf * PT;
@@ -802,7 +805,7 @@ __global__ void __launch_bounds__(S_THREADS, NC == 1 || !CHAINS ? 2 : 1)
     uint32_t phase = 1;
     for (; i < nk; ++i) {
       if (!mbar_wait(&empty[s], phase)) {
-        atomicOr(&g_lin_status, STATUS_TIMEOUT);
+        report_timeout();
         break;
       }
       uint8_t* a = smem + s * stage;
@@ -854,7 +857,7 @@ __global__ void __launch_bounds__(S_THREADS, NC == 1 || !CHAINS ? 2 : 1)
         __syncwarp();
       }
     }
-    if (!ok) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    if (!ok) report_timeout();
     __syncwarp();
     if (elect_one()) umma_commit(done);
     __syncwarp();
@@ -888,9 +891,9 @@ __global__ void __launch_bounds__(S_THREADS, NC == 1 || !CHAINS ? 2 : 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ch_empty[buf]);
       }
-      if (!ok && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+      if (!ok && lane == 0) report_timeout();
     }
-    if (!__all_sync(0xffffffffu, mbar_wait(done, 0)) && lane == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    if (!__all_sync(0xffffffffu, mbar_wait(done, 0)) && lane == 0) report_timeout();
   }
   // All copies have landed and all MMAs have read them: the ring becomes the
   // partial tile part[row][128 columns].  Lane l of quadrant q holds column
@@ -935,7 +938,7 @@ __global__ void __launch_bounds__(S_THREADS, NC == 1 || !CHAINS ? 2 : 1)
       }
     }
     __syncwarp();
-    if (!mbar_wait_cl(arrived, 0) && threadIdx.x == 0) atomicOr(&g_lin_status, STATUS_TIMEOUT);
+    if (!mbar_wait_cl(arrived, 0) && threadIdx.x == 0) report_timeout();
     __syncwarp();
     // (what this CTA receives has arrived; when all say so, all copies are done)
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -1171,6 +1174,16 @@ __global__ void __launch_bounds__(256)
     for (int i = 0; i < 8; ++i) t += red[i][cl];
     out[c] = from_f<O>(t);
   }
+}
+
+// A wait that nothing ends, over at once: 64 tests of a barrier with no arrivals.
+__global__ void k_expire() {
+  __shared__ uint64_t bar;
+  if (threadIdx.x == 0) mbar_init(&bar, 1);
+  __syncthreads();
+  bool done = false;
+  for (uint32_t i = 0; i < WAIT_SPIN && !done; ++i) done = mbar_test_wait(&bar, 0);
+  if (!done && threadIdx.x == 0) report_timeout();
 }
 
 // -------------------------------------------------------------------- host --
@@ -1628,13 +1641,20 @@ extern "C" mpq_status mpq_linear_backward(const void* dy, int64_t ldy, const voi
 }
 
 extern "C" mpq_status mpq_ops_status(mpq_stream_t stream) {
+  static thread_local uint32_t seen[64] = {};
   cudaStream_t st = (cudaStream_t)stream;
-  int word = 0;
-  MPQ_CUDA(cudaMemcpyFromSymbolAsync(&word, g_lin_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st));
+  int dev = 0, sms = 0;
+  MPQ_TRY(current_device(&dev, &sms));
+  uint32_t now = 0;
+  MPQ_CUDA(cudaMemcpyFromSymbolAsync(&now, g_timeouts, sizeof(now), 0, cudaMemcpyDeviceToHost, st));
   MPQ_CUDA(cudaStreamSynchronize(st));
-  if (!word) return MPQ_OK;
-  static const int zero = 0;
-  MPQ_CUDA(cudaMemcpyToSymbolAsync(g_lin_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st));
-  MPQ_CUDA(cudaStreamSynchronize(st));
+  if (now == seen[dev]) return MPQ_OK;
+  seen[dev] = now;
   return fail(MPQ_ERR_TIMEOUT, "a bounded wait of a linear kernel ran out");
+}
+
+extern "C" mpq_status mpq_ops_expire(mpq_stream_t stream) {
+  k_expire<<<1, 32, 0, (cudaStream_t)stream>>>();
+  count_launch();
+  return check_launch("k_expire");
 }

@@ -365,6 +365,7 @@ def topk_distill(logits: torch.Tensor, top_logits: torch.Tensor, top_ids: torch.
 
 def ops_status(device=None):
     """Synchronise the current stream; raise MPQError if a kernel of these
-    operators ran out of a bounded wait since the last call."""
+    operators ran out of a bounded wait, on any stream of the device, since this
+    thread's last call."""
     with torch.cuda.device(device):
         check(lib.mpq_ops_status(torch.cuda.current_stream().cuda_stream), "mpq_ops_status")
