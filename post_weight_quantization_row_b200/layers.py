@@ -7,7 +7,8 @@ and limits stand in include/mpq.h); this module checks arguments, allocates
 outputs and scratch on the inputs' device and passes the current stream of that
 device.  The calls neither synchronise nor keep anything, and can be captured
 into CUDA graphs.  Gradients are functions of their own: nothing here takes
-part in autograd.
+part in autograd, and a forward call whose inputs require a gradient outside
+torch.no_grad() warns that its results do not carry it.
 
 Tensors of any rank count as rows of their last dimension, which must be
 contiguous; the rows must lie at one distance from each other (any slice
@@ -17,6 +18,7 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+import warnings
 from typing import Optional
 
 import torch
@@ -82,6 +84,15 @@ def _vector(t: torch.Tensor, dtype, shape, like: torch.Tensor, name: str):
     return t.data_ptr()
 
 
+def _detached(name: str, *inputs):
+    """Warns where autograd would expect a gradient that no result carries."""
+    for t in inputs:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            warnings.warn(f"{name} takes no part in autograd: no gradient will reach its inputs by backward().  Use the "
+                          "gradients that the package computes, and torch.no_grad() around this call.", stacklevel=3)
+            return
+
+
 def _act(name: str) -> int:
     if name not in ACTIVATIONS:
         raise ValueError(f"unknown activation {name!r}; one of {', '.join(ACTIVATIONS)}")
@@ -132,6 +143,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     linear_backward.
     """
     act = _act(activation)
+    _detached("linear", x, weight, bias, residual)
     _half_operand(x, "x")
     rows, k, ldx = _rows(x, "x")
     if weight.dim() != 2 or weight.dtype != x.dtype:
@@ -239,6 +251,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     """
     if x.dtype not in DTYPES:
         raise ValueError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    _detached("layer_norm", x, weight, bias)
     rows, n, ldx = _rows(x, "x")
     if n < 1:
         raise ValueError("x has no columns")
@@ -308,6 +321,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     """
     if logits.dtype not in DTYPES:
         raise ValueError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    _detached("token_logprobs", logits)
     rows, v, ldl = _rows(logits, "logits")
     if v < 1:
         raise ValueError("logits have no columns")
@@ -342,6 +356,7 @@ def topk_distill(logits: torch.Tensor, top_logits: torch.Tensor, top_ids: torch.
     """
     if logits.dtype not in DTYPES:
         raise ValueError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    _detached("topk_distill", logits, top_logits)
     rows, v, ldl = _rows(logits, "logits")
     if v < 1:
         raise ValueError("logits have no columns")
