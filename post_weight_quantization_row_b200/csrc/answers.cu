@@ -486,7 +486,6 @@ struct DistillArgs {
 struct TeacherShared {
   float q[MPQ_TOP_MAX], logq[MPQ_TOP_MAX];
   int id[MPQ_TOP_MAX];  // -1: padding
-  float logsum, mx;
   int bad, live;
 };
 
@@ -651,7 +650,7 @@ int row_ctas(int64_t rows, int64_t v, int sms) {
 }
 
 template <typename A>
-mpq_status launch_rows(void (*one)(A), void (*many)(A), const A& a, int threads, cudaStream_t st, const char* name) {
+mpq_status launch_rows(void (*kernel)(A), const A& a, int threads, cudaStream_t st, const char* name) {
   const int C = a.C;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * C));
@@ -665,7 +664,7 @@ mpq_status launch_rows(void (*one)(A), void (*many)(A), const A& a, int threads,
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
   ProfScope ps_(name, st);
-  MPQ_CUDA(cudaLaunchKernelEx(&cfg, C > 1 ? many : one, a));
+  MPQ_CUDA(cudaLaunchKernelEx(&cfg, kernel, a));
   count_launch();
   return check_launch(name);
 }
@@ -673,29 +672,29 @@ mpq_status launch_rows(void (*one)(A), void (*many)(A), const A& a, int threads,
 // Whether four CTAs an SM, a row each, would hold more than L2 does: then two of
 // twice the threads.
 template <typename T>
-bool large_rows(int C, int64_t v) {
-  return C == 1 && 4ll * 148 * v * (int64_t)sizeof(T) > L2_ROWS;
+bool large_rows(int C, int64_t v, int sms) {
+  return C == 1 && 4ll * sms * v * (int64_t)sizeof(T) > L2_ROWS;
 }
 
 template <typename T>
-mpq_status run_logprobs(const LogprobArgs& a, cudaStream_t st) {
+mpq_status run_logprobs(const LogprobArgs& a, int sms, cudaStream_t st) {
   // (the columns that are read again should still be in L2: 1024 rows of
   // 131072 bf16 with 64 alternatives take 92 us with 512 threads, 104 with 256;
   // 4096 rows of 32000 with 20 take 125 and 101)
-  if (a.top && large_rows<T>(a.C, a.v))
-    return launch_rows(k_token_logprobs<512, T, true, false>, k_token_logprobs<512, T, true, true>, a, 512, st, "k_token_logprobs");
-  if (a.top) return launch_rows(k_token_logprobs<256, T, true, false>, k_token_logprobs<256, T, true, true>, a, 256, st, "k_token_logprobs");
-  return launch_rows(k_token_logprobs<256, T, false, false>, k_token_logprobs<256, T, false, true>, a, 256, st, "k_token_logprobs");
+  if (a.top && large_rows<T>(a.C, a.v, sms))
+    return launch_rows(k_token_logprobs<512, T, true, false>, a, 512, st, "k_token_logprobs");
+  const bool cl = a.C > 1;
+  if (a.top) return launch_rows(cl ? k_token_logprobs<256, T, true, true> : k_token_logprobs<256, T, true, false>, a, 256, st, "k_token_logprobs");
+  return launch_rows(cl ? k_token_logprobs<256, T, false, true> : k_token_logprobs<256, T, false, false>, a, 256, st, "k_token_logprobs");
 }
 template <typename T>
-mpq_status run_distill(const DistillArgs& a, cudaStream_t st) {
+mpq_status run_distill(const DistillArgs& a, int sms, cudaStream_t st) {
   // the second reading of a row should find it in L2 (1024 rows of 131072
   // bf16, 20 entries, in row order: 132 us with 512 threads, 144 with 256; from
   // the row's end with streaming stores 125; 4096 rows of 32000: 139 with 512,
   // 121 with 256.  Clusters of 2 and 4 CTAs a row: 137 to 181, 169 to 450)
-  const bool large = a.dlogits && large_rows<T>(a.C, a.v);
-  if (large) return launch_rows(k_topk_distill<512, T, false>, k_topk_distill<512, T, true>, a, 512, st, "k_topk_distill");
-  return launch_rows(k_topk_distill<256, T, false>, k_topk_distill<256, T, true>, a, 256, st, "k_topk_distill");
+  if (a.dlogits && large_rows<T>(a.C, a.v, sms)) return launch_rows(k_topk_distill<512, T, false>, a, 512, st, "k_topk_distill");
+  return launch_rows(a.C > 1 ? k_topk_distill<256, T, true> : k_topk_distill<256, T, false>, a, 256, st, "k_topk_distill");
 }
 
 mpq_status rows_check(const char* who, int64_t rows, int64_t v, int32_t dtype) {
@@ -740,9 +739,9 @@ extern "C" mpq_status mpq_token_logprobs(const void* logits, int64_t ldl, int64_
   a.top_logprob = top_logprob;
   a.top_id = top_id;
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == MPQ_BF16) return run_logprobs<__nv_bfloat16>(a, st);
-  if (dtype == MPQ_F16) return run_logprobs<__half>(a, st);
-  return run_logprobs<float>(a, st);
+  if (dtype == MPQ_BF16) return run_logprobs<__nv_bfloat16>(a, sms, st);
+  if (dtype == MPQ_F16) return run_logprobs<__half>(a, sms, st);
+  return run_logprobs<float>(a, sms, st);
 }
 
 extern "C" mpq_status mpq_topk_distill(const void* logits, int64_t ldl, int64_t rows, int64_t v, int32_t dtype,
@@ -775,7 +774,7 @@ extern "C" mpq_status mpq_topk_distill(const void* logits, int64_t ldl, int64_t 
   a.loss = loss;
   a.dlogits = dlogits;
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == MPQ_BF16) return run_distill<__nv_bfloat16>(a, st);
-  if (dtype == MPQ_F16) return run_distill<__half>(a, st);
-  return run_distill<float>(a, st);
+  if (dtype == MPQ_BF16) return run_distill<__nv_bfloat16>(a, sms, st);
+  if (dtype == MPQ_F16) return run_distill<__half>(a, sms, st);
+  return run_distill<float>(a, sms, st);
 }

@@ -126,12 +126,6 @@ __device__ __forceinline__ void load_param(const void* p, bool f32, int64_t at, 
   if (f32) load_edge<W>(static_cast<const float*>(p) + at, v, n, vec);
   else load_edge<W>(static_cast<const T*>(p) + at, v, n, vec);
 }
-template <int W, typename T>
-__device__ __forceinline__ void store_param(void* p, bool f32, int64_t at, const float (&v)[W],
-                                            int n, bool vec) {
-  if (f32) store_edge<W>(static_cast<float*>(p) + at, v, n, vec);
-  else store_edge<W>(static_cast<T*>(p) + at, v, n, vec);
-}
 
 // 8 consecutive elements as they lie in memory: half the registers of floats
 // for 16-bit types.
