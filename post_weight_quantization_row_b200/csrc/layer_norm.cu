@@ -24,7 +24,7 @@
 namespace mpq {
 namespace {
 
-constexpr int LN_BACK_BLOCKS = 1184;       // partial rows of dw and db at most
+constexpr int64_t LN_BACK_BLOCKS = 1184;       // partial rows of dw and db at most
 constexpr int64_t LN_REG_MAX = 32768;      // widest row held in registers (forward)
 constexpr int LN_PART = 8192;              // columns per CTA of the backward kernel
 constexpr int64_t LN_BACK_MAX = 4 * LN_PART;  // widest row of a cluster of them
@@ -74,6 +74,7 @@ struct LnArgs {
   const void* b;
   bool p_f32, x_vec, p_vec, o_vec;
   int G, C;
+  int sms;  // of the device
 };
 
 // How rows and parameters come.  Parameters: none, all in T, all in fp32, on
@@ -612,7 +613,7 @@ void ln_fwd_rows(LnArgs a, float e, T* y, float* mean, float* rstd, cudaStream_t
   // One vector a thread where there are too few rows to fill the device with
   // small groups; 4 otherwise: a row of 4096 then has one barrier between 4
   // warps per sum, and 8 rows are at work on an SM.
-  const bool few = a.rows * cdiv(a.n, 1024) < 148 * 8;
+  const bool few = a.rows * cdiv(a.n, 1024) < 8 * a.sms;
   if (few && a.n <= 8192) go(k_ln_fwd<T, 1, 1, PM>, 1, 1);
   else if (a.n <= 256) go(k_ln_fwd<T, 1, 4, PM>, 1, 4);
   else if (a.n <= 512) go(k_ln_fwd<T, 2, 2, PM>, 2, 2);
@@ -650,7 +651,8 @@ mpq_status ln_bwd_rows(LnArgs a, const T* dy, int64_t ldy, const float* mean, co
     a.G = a.C > 1 ? LN_PART / 16 : group_threads(a.n, nv, 4);
     const int block = a.G > 32 ? a.G : 128;
     const int64_t groups = block / a.G;
-    *blocks = std::min<int64_t>(cdiv(a.rows, groups), 148 * std::max(1, std::min(8, 512 / block)) / a.C);
+    *blocks = std::min<int64_t>({cdiv(a.rows, groups), (int64_t)a.sms * std::max(1, std::min(8, 512 / block)) / a.C,
+                                 LN_BACK_BLOCKS});  // (the workspace has no more partial rows)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(*blocks * a.C));
     cfg.blockDim = dim3(block);
@@ -752,6 +754,8 @@ extern "C" mpq_status mpq_layer_norm(const void* x, int64_t ldx, int64_t rows, i
   const int64_t es = dtype_size(dtype), ps = dtype_size(param_dtype);
   MPQ_TRY(check_elements("layer_norm", {{x, es}, {y, es}, {weight, ps}, {bias, ps}, {mean, 4}, {rstd, 4}}));
   LnArgs a{};
+  int dev = 0;
+  MPQ_TRY(current_device(&dev, &a.sms));
   a.x = x;
   a.ldx = ldx;
   a.rows = rows;
@@ -798,6 +802,8 @@ extern "C" mpq_status mpq_layer_norm_backward(const void* dy, int64_t ldy, const
     return fail(MPQ_ERR_INVALID_ARG, "layer_norm_backward: needs " + std::to_string(need) +
                                          " bytes of workspace on a 256-byte boundary");
   LnArgs a{};
+  int dev = 0;
+  MPQ_TRY(current_device(&dev, &a.sms));
   a.x = x;
   a.ldx = ldx;
   a.rows = rows;

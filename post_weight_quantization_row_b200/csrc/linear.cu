@@ -1229,6 +1229,7 @@ int64_t tma_ld(const Operand& a) { return a.rows <= 1 ? round_up(a.inner, 8) : a
 
 // Packs those of two operands that have somewhere to go.
 mpq_status pack(Operand* a, void* dst_a, Operand* b, void* dst_b, cudaStream_t st) {
+  int dev = 0, sms = 0;
   const auto job = [](Operand* q, void* dst) {
     PackJob j{};
     if (!dst) return j;
@@ -1240,9 +1241,10 @@ mpq_status pack(Operand* a, void* dst_a, Operand* b, void* dst_b, cudaStream_t s
   const PackJob ja = job(a, dst_a), jb = job(b, dst_b);
   const int64_t work = (ja.rows * ja.ldd + jb.rows * jb.ldd) / 8;
   if (work == 0) return MPQ_OK;
+  MPQ_TRY(current_device(&dev, &sms));
   {
     ProfScope ps_("k_lin_pack", st);
-    k_lin_pack<<<(unsigned)std::min<int64_t>(cdiv(work, 256), 148 * 16), 256, 0, st>>>(ja, jb);
+    k_lin_pack<<<(unsigned)std::min<int64_t>(cdiv(work, 256), sms * 16), 256, 0, st>>>(ja, jb);
   }
   count_launch();
   return check_launch("k_lin_pack");
@@ -1452,8 +1454,9 @@ mpq_status linear_fwd(Operand x, Operand w, const LinOut& o, char* ws, cudaStrea
   if (use_gemv(x, w)) {
     // a warp per row of W fills the device from 24 warps an SM on; below that
     // more warps share a row, as long as each has 512 elements
-    int wpr = 1;
-    while (wpr < GEMV_WARPS && w.rows * wpr < 148 * 24 && x.inner >= 1024 * wpr) wpr *= 2;
+    int wpr = 1, dev = 0, sms = 0;
+    MPQ_TRY(current_device(&dev, &sms));
+    while (wpr < GEMV_WARPS && w.rows * wpr < sms * 24 && x.inner >= 1024 * wpr) wpr *= 2;
     const unsigned grid = (unsigned)cdiv(w.rows, GEMV_WARPS / wpr);
     const bool vec = aligned_rows(x.p, x.ld, 2, 16) && aligned_rows(w.p, w.ld, 2, 16);
     const auto go = [&](auto kernel) {
