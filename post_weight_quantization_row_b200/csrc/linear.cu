@@ -1332,7 +1332,7 @@ mpq_status lin_device(int* dev_out, int* sms_out) {
 
 // Geometry of the split kernel.  Tiles of up to 32 rows leave room for two
 // CTAs on an SM; the contraction is split while that finds free SMs and each
-// CTA keeps 4 steps.  Clusters of 8 only where they leave half of the SMs
+// CTA keeps 2 steps.  Clusters of 8 only where they leave half of the SMs
 // free: 16 of them (256 x 1024 over 2048) find no place at once and take 18.7
 // us, clusters of 4 11.0.
 SplitGeom split_geom(const LinOut& o, bool rows_mn, int64_t KT, int sms, int chain) {
