@@ -17,6 +17,7 @@
 // Rows that start at odd addresses pay for shifting their vectors: 2000 x 5001
 // bf16 takes 21 us and 60 us.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "layer_ops.cuh"
@@ -727,15 +728,15 @@ mpq_status ln_bwd(LnArgs a, const void* dy, int64_t ldy, bool y_vec, const float
 }  // namespace
 
 mpq_status current_device(int* dev, int* sms) {
-  static int cached[64] = {};
+  static std::atomic<int> cached[64] = {};  // (host threads may call at once)
   MPQ_CUDA(cudaGetDevice(dev));
   if (*dev < 0 || *dev >= 64) return fail(MPQ_ERR_CUDA, "device index out of range");
-  if (!cached[*dev]) {
-    int n = 0;
+  int n = cached[*dev].load(std::memory_order_relaxed);
+  if (!n) {
     MPQ_CUDA(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev));
-    cached[*dev] = n;
+    cached[*dev].store(n, std::memory_order_relaxed);
   }
-  *sms = cached[*dev];
+  *sms = n;
   return MPQ_OK;
 }
 
