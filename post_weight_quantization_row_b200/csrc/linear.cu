@@ -19,9 +19,10 @@
 // The epilogue adds the bias, applies the activation, adds the residual and
 // rounds once, in fp32 before that.
 //
-// Measured: 4096 x 14336 -> 4096 bf16 with a residual takes 297 to 335 us,
-// with the power that the device has left (1.44 to 1.62 PFLOP/s; the tensor
-// pipe active in 92% of the cycles); its backward products the same rate.  One
+// Measured: 4096 x 14336 -> 4096 bf16 with a residual takes 300 to 337 us in a
+// replayed graph (1.43 to 1.60 PFLOP/s; the tensor pipe active in 91% of the
+// cycles) and 395 in a long loop of calls, where the power cap lowers the clock;
+// with an fp32 result 338 to 363; its backward products run at the same rate.  One
 // row of 4096 -> 4096: 9.0 us for the 33.6 MB of W (3.7 TB/s; at the
 // copy rate 5.1).  In between the fixed part of a launch counts:
 // 256 x 2048 -> 512 takes 10.9.
